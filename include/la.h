@@ -266,6 +266,64 @@ la_status la_qkv_state(const la_shape* shape, int C, const void* X,
                        const void* W, const void* bias, void* Q, float* S,
                        float* z, void* ws, size_t ws_bytes, la_stream stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators of a causal block: gated linear attention, rotary positions, and
+ * the gated residual with the norms around it. They follow the conventions
+ * above, except that their workspaces need no zero fill.
+ */
+
+/* Shape of gated linear attention. Q, K, V, O and their gradients are dense
+ * [B, N, H, D] tensors of io_dtype, G and its gradient dense [B, N, H] float32,
+ * states dense [B, H, D, D] float32 (row: dimension of k, column: of v). */
+typedef struct {
+  int B, N, H;  /* batch elements, tokens, heads; >= 0 */
+  int D;        /* head width; must be 32 */
+  int io_dtype; /* LA_IO_BF16 or LA_IO_F32 */
+  float scale;  /* factor of the queries, finite */
+} la_gated_shape;
+
+/* Bytes of workspace la_gated_attention (backward = 0) or
+ * la_gated_attention_backward (backward = 1) needs. 0 iff the shape is invalid.
+ * Pure host function. */
+size_t la_gated_workspace_bytes(const la_gated_shape* shape, int backward);
+
+/* Gated linear attention: token-causal, with a decay per token and head,
+ *   S_n = exp(g_n) S_{n-1} + k_n^T v_n,   o_n = scale q_n S_n,   S_{-1} = S_in.
+ * Without feature map or normaliser: apply a feature map to q and k before, a
+ * norm to o after. G holds the log gates g <= 0. A gate below -104 (-inf
+ * included) lets nothing through: the state starts anew at that token, which
+ * packs several sequences into one row (the first token of each has g = -inf).
+ * Larger gates are summed as they are, g > 0 lets the state grow. S_in NULL: a
+ * zero state. S_out (may be NULL) receives the last state; it may be S_in
+ * itself, so a sequence can be fed in pieces of any length (prompt, then one
+ * token at a time). N = 0 copies S_in to S_out. A NaN or infinity in q, k, v or
+ * G may reach the outputs of all tokens of its 16-token block and later ones.
+ * float32 sums and state; bf16 outputs are rounded once. Up to 8 tokens run as
+ * one launch that walks them one by one; longer calls walk 16-token blocks on
+ * the tensor cores, in one launch where B*H fills the GPU, else in three
+ * (segments' states, their combination, the segments). Deterministic.
+ * O must not overlap an input, S_out or the workspace; S_out must not overlap
+ * an input other than being S_in, nor the workspace. */
+la_status la_gated_attention(const la_gated_shape* shape, const void* Q, const void* K,
+                             const void* V, const float* G, const float* S_in, float* S_out,
+                             void* O, void* ws, size_t ws_bytes, la_stream stream);
+
+/* Backward of la_gated_attention. dO: [B,N,H,D] io_dtype, the gradient of O;
+ * dS_out: [B,H,D,D] float32, the gradient of S_out, or NULL for zero. With
+ * U_n = sum_{i>=n} exp(g_{n+1} + .. + g_i) scale q_i^T dO_i (+ dS_out, decayed):
+ *   dq_n = scale S_n dO_n,  dk_n = U_n v_n,  dv_n = k_n U_n,
+ *   dg_n = <exp(g_n) U_n, S_{n-1}>,  dS_in = exp(g_0) U_0.
+ * dQ, dK, dV: io_dtype; dG: [B,N,H] float32 (0 at gates below -104); dS_in: [B,H,D,D]
+ * float32 or NULL. S_in as the forward had it (S_out must not have been written
+ * over it). Recomputes the states; two launches, four where the sequence is cut
+ * into segments. Deterministic. No output may overlap another, an input or the
+ * workspace. */
+la_status la_gated_attention_backward(const la_gated_shape* shape, const void* Q, const void* K,
+                                      const void* V, const float* G, const float* S_in,
+                                      const void* dO, const float* dS_out, void* dQ, void* dK,
+                                      void* dV, float* dG, float* dS_in, void* ws,
+                                      size_t ws_bytes, la_stream stream);
+
 /* Reset of the KV cache at the start of a video (SANA-Video section 4: the
  * cache starts empty): S[B,H,D,D] = 0, z[B,H,D] = 0 on `stream`. */
 la_status la_state_reset(float* S, float* z, int B, int H, int D,

@@ -52,6 +52,15 @@ class LaConvShape(ctypes.Structure):
     ]
 
 
+class LaGatedShape(ctypes.Structure):
+    """Mirror of ``la_gated_shape`` in include/la.h."""
+
+    _fields_ = [
+        ("B", ctypes.c_int), ("N", ctypes.c_int), ("H", ctypes.c_int), ("D", ctypes.c_int),
+        ("io_dtype", ctypes.c_int), ("scale", ctypes.c_float),
+    ]
+
+
 class LaError(RuntimeError):
     def __init__(self, status: int, func: str):
         self.status = status
@@ -88,6 +97,13 @@ _lib.la_qkv_workspace_bytes.argtypes = [_shape_p, _i]
 _lib.la_qkv_workspace_bytes.restype = _sz
 _lib.la_qkv_state.argtypes = [_shape_p, _i] + [_vp] * 7 + [_sz, _vp]
 _lib.la_qkv_state.restype = _i
+_gated_p = ctypes.POINTER(LaGatedShape)
+_lib.la_gated_workspace_bytes.argtypes = [_gated_p, _i]
+_lib.la_gated_workspace_bytes.restype = _sz
+_lib.la_gated_attention.argtypes = [_gated_p] + [_vp] * 8 + [_sz, _vp]
+_lib.la_gated_attention.restype = _i
+_lib.la_gated_attention_backward.argtypes = [_gated_p] + [_vp] * 13 + [_sz, _vp]
+_lib.la_gated_attention_backward.restype = _i
 _lib.la_state_reset.argtypes = [_vp, _vp, _i, _i, _i, _vp]
 _lib.la_state_reset.restype = _i
 _lib.la_status_string.argtypes = [_i]
@@ -217,6 +233,33 @@ def la_qkv_state(shape: LaShape, C: int, X, W, bias, Q, S, z, ws, stream=None) -
     _check(_lib.la_qkv_state(ctypes.byref(shape), int(C), _ptr(X), _ptr(W), _ptr(bias), _ptr(Q),
                              _ptr(S), _ptr(z), _ptr(ws), _nbytes(ws), _stream(stream)),
            "la_qkv_state")
+
+
+def make_gated_shape(B: int, N: int, H: int, D: int = HEAD_DIM, io_dtype: str = "bf16",
+                     scale: float = 1.0) -> LaGatedShape:
+    io = {"bf16": LA_IO_BF16, "f32": LA_IO_F32, "float32": LA_IO_F32}[io_dtype]
+    return LaGatedShape(int(B), int(N), int(H), int(D), io, float(scale))
+
+
+def la_gated_workspace_bytes(shape: LaGatedShape, backward: bool = False) -> int:
+    return int(_lib.la_gated_workspace_bytes(ctypes.byref(shape), int(bool(backward))))
+
+
+def la_gated_attention(shape: LaGatedShape, Q, K, V, G, S_in, S_out, O, ws, stream=None) -> None:
+    """Gated linear attention; S_in, S_out may be None, S_out may be S_in (see include/la.h)."""
+    _check(_lib.la_gated_attention(ctypes.byref(shape), _ptr(Q), _ptr(K), _ptr(V), _ptr(G),
+                                   _ptr(S_in), _ptr(S_out), _ptr(O), _ptr(ws), _nbytes(ws),
+                                   _stream(stream)), "la_gated_attention")
+
+
+def la_gated_attention_backward(shape: LaGatedShape, Q, K, V, G, S_in, dO, dS_out, dQ, dK, dV,
+                                dG, dS_in, ws, stream=None) -> None:
+    """Gradients of la_gated_attention; S_in, dS_out, dS_in may be None."""
+    _check(_lib.la_gated_attention_backward(ctypes.byref(shape), _ptr(Q), _ptr(K), _ptr(V),
+                                            _ptr(G), _ptr(S_in), _ptr(dO), _ptr(dS_out),
+                                            _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(dG), _ptr(dS_in),
+                                            _ptr(ws), _nbytes(ws), _stream(stream)),
+           "la_gated_attention_backward")
 
 
 def la_state_reset(S, z, B: int, H: int, D: int = HEAD_DIM, stream=None) -> None:
@@ -349,3 +392,100 @@ def qkv_state(X, W, bias=None, rope_grid=None, t_offset: int = 0, rope_base: flo
     ws = torch.empty(n, dtype=torch.uint8, device=X.device)
     la_qkv_state(shape, C, X, W, bias, Q, S, z, ws, stream)
     return Q, S, z
+
+
+# Gated linear attention, rotary positions, gated residual with norms. These
+# wrappers check every tensor, run on the tensors' own device (on its current
+# stream unless one is given) and take their workspace from torch's allocator.
+
+def _io_of(x, name: str) -> str:
+    import torch
+    if x.dtype == torch.bfloat16:
+        return "bf16"
+    if x.dtype == torch.float32:
+        return "f32"
+    raise ValueError(f"{name} must be bfloat16 or float32, got {x.dtype}")
+
+
+def _need(name: str, x, shape, dtype, device) -> None:
+    """Raise ValueError unless x (None is left to the caller) is a contiguous tensor of this
+    shape, type and device."""
+    if x is None:
+        return
+    if x.device != device or x.dtype != dtype or x.shape != shape or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}, got "
+                         f"{x.dtype} {tuple(x.shape)} with strides {x.stride()} on {x.device}")
+
+
+class _On:
+    """The tensors' device as the current one, and the stream to launch on."""
+
+    def __init__(self, device, stream):
+        import torch
+        if device.type != "cuda":
+            raise ValueError("tensor arguments must live on a CUDA device")
+        self._guard = None
+        if device.index != torch.cuda.current_device():
+            self._guard = torch.cuda.device(device)
+        self.stream = torch.cuda.current_stream(device).cuda_stream if stream is None else stream
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+        return False
+
+
+def _gated_checks(Q, K, V, G, **states):
+    import torch
+    if Q.dim() != 4 or Q.shape[-1] != HEAD_DIM:
+        raise ValueError(f"Q must be [B, N, H, {HEAD_DIM}], got {tuple(Q.shape)}")
+    io = _io_of(Q, "Q")
+    B, N, H, D = Q.shape
+    for name, x in (("Q", Q), ("K", K), ("V", V)):
+        _need(name, x, Q.shape, Q.dtype, Q.device)
+    _need("G", G, (B, N, H), torch.float32, Q.device)
+    for name, x in states.items():
+        _need(name, x, (B, H, D, D), torch.float32, Q.device)
+    return io
+
+
+def gated_attention(Q, K, V, G, S_in=None, scale: float = 1.0, want_state: bool = False, S_out=None,
+                    stream=None):
+    """O (and the last state when ``want_state`` or ``S_out`` is given) of gated linear attention:
+    S_n = exp(g_n) S_{n-1} + k_n^T v_n, o_n = scale q_n S_n, for [B, N, H, 32] CUDA tensors and
+    log gates G [B, N, H] float32. ``S_out`` may be ``S_in``: the state is then updated in place."""
+    import torch
+    io = _gated_checks(Q, K, V, G, S_in=S_in, S_out=S_out)
+    B, N, H, D = Q.shape
+    shape = LaGatedShape(B, N, H, D, LA_IO_BF16 if io == "bf16" else LA_IO_F32, scale)
+    with _On(Q.device, stream) as st:
+        O = torch.empty_like(Q)
+        if S_out is None and want_state:
+            S_out = torch.empty((B, H, D, D), dtype=torch.float32, device=Q.device)
+        ws = torch.empty(la_gated_workspace_bytes(shape), dtype=torch.uint8, device=Q.device)
+        la_gated_attention(shape, Q, K, V, G, S_in, S_out, O, ws, st)
+    return O if S_out is None else (O, S_out)
+
+
+def gated_attention_backward(Q, K, V, G, dO, S_in=None, dS_out=None, scale: float = 1.0,
+                             want_state: Optional[bool] = None, stream=None):
+    """dQ, dK, dV, dG, dS_in of gated_attention. dS_in is None unless ``want_state`` (by default:
+    where an S_in is given); S_in must still hold the state that the forward began with."""
+    import torch
+    io = _gated_checks(Q, K, V, G, S_in=S_in, dS_out=dS_out)
+    _need("dO", dO, Q.shape, Q.dtype, Q.device)
+    B, N, H, D = Q.shape
+    shape = LaGatedShape(B, N, H, D, LA_IO_BF16 if io == "bf16" else LA_IO_F32, scale)
+    if want_state is None:
+        want_state = S_in is not None
+    with _On(Q.device, stream) as st:
+        dQ, dK, dV, dG = (torch.empty_like(x) for x in (Q, K, V, G))
+        dS = torch.empty((B, H, D, D), dtype=torch.float32, device=Q.device) if want_state else None
+        ws = torch.empty(la_gated_workspace_bytes(shape, True), dtype=torch.uint8, device=Q.device)
+        la_gated_attention_backward(shape, Q, K, V, G, S_in, dO, dS_out, dQ, dK, dV, dG, dS, ws, st)
+    return dQ, dK, dV, dG, dS

@@ -1,0 +1,168 @@
+// C-ABI layer of the block operators of include/la.h: gated linear attention,
+// rotary positions, the gated residual with its norms.
+#include <cmath>
+
+#include "la.h"
+#include "la_block_internal.h"
+#include "la_internal.h"
+
+using namespace la;
+using namespace la::detail;
+
+namespace {
+
+#define LA_TRY(expr)              \
+  do {                            \
+    const la_status st_ = (expr); \
+    if (st_ != LA_OK) return st_; \
+  } while (0)
+
+struct Buffer {
+  const void* p;
+  size_t n;
+  const char* name;
+};
+
+// Outputs must not overlap each other or an input.
+template <size_t kOut, size_t kIn>
+la_status check_apart(const Buffer (&outs)[kOut], const Buffer (&ins)[kIn]) {
+  for (size_t i = 0; i < kOut; ++i) {
+    for (size_t j = i + 1; j < kOut; ++j)
+      if (overlap(outs[i].p, outs[i].n, outs[j].p, outs[j].n))
+        return fail(LA_ERR_INVALID_ARG, "%s and %s overlap", outs[i].name, outs[j].name);
+    for (size_t j = 0; j < kIn; ++j)
+      if (overlap(outs[i].p, outs[i].n, ins[j].p, ins[j].n))
+        return fail(LA_ERR_INVALID_ARG, "%s and %s overlap", outs[i].name, ins[j].name);
+  }
+  return LA_OK;
+}
+
+la_status check_workspace(const void* ws, size_t ws_bytes, size_t need) {
+  if (need == 0) return LA_OK;
+  if (ws == nullptr) return fail(LA_ERR_WORKSPACE, "workspace is NULL (need %zu bytes)", need);
+  LA_TRY(check_ptr(ws, "workspace", true));
+  if (ws_bytes < need)
+    return fail(LA_ERR_WORKSPACE, "workspace of %zu bytes < %zu needed", ws_bytes, need);
+  return LA_OK;
+}
+
+la_status make_gated(const la_gated_shape* s, bool backward, GatedProblem& p) {
+  if (s == nullptr) return fail(LA_ERR_INVALID_ARG, "shape is NULL");
+  if (s->B < 0 || s->N < 0 || s->H < 0)
+    return fail(LA_ERR_INVALID_ARG, "negative size B=%d N=%d H=%d", s->B, s->N, s->H);
+  if (s->D != kD) return fail(LA_ERR_UNSUPPORTED, "head width D=%d (only 32 is built)", s->D);
+  if (s->io_dtype != LA_IO_BF16 && s->io_dtype != LA_IO_F32)
+    return fail(LA_ERR_INVALID_ARG, "io_dtype=%d", s->io_dtype);
+  if (!std::isfinite(s->scale)) return fail(LA_ERR_INVALID_ARG, "scale must be finite");
+  if (s->B > 65535 || s->H > 65535 || 1LL * s->B * s->H > (1LL << 24) || s->N > (1 << 30))
+    return fail(LA_ERR_UNSUPPORTED, "B=%d, H=%d or N=%d too large", s->B, s->H, s->N);
+  if (1.0 * s->B * s->N * s->H >= 1.0 * (1LL << 35))
+    return fail(LA_ERR_UNSUPPORTED, "tensor too large");
+  p.B = s->B;
+  p.N = s->N;
+  p.H = s->H;
+  p.io = s->io_dtype;
+  p.scale = s->scale;
+  gated_split(p, backward);
+  return LA_OK;
+}
+
+size_t gated_need(const GatedProblem& p, bool backward) {
+  if (p.B == 0 || p.H == 0 || p.N == 0) return 0;
+  if (!backward && p.N <= kGateStepTokens) return 0;
+  return align256(gated_workspace_floats(p, backward) * sizeof(float));
+}
+
+// dst = src, or zero without src (an empty sequence passes its state on).
+la_status pass_on(float* dst, const float* src, size_t bytes, cudaStream_t st) {
+  if (dst == nullptr || dst == src) return LA_OK;
+  const cudaError_t e = src != nullptr
+                            ? cudaMemcpyAsync(dst, src, bytes, cudaMemcpyDeviceToDevice, st)
+                            : cudaMemsetAsync(dst, 0, bytes, st);
+  return e == cudaSuccess ? LA_OK : cuda_fail(e, "state of an empty sequence");
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t la_gated_workspace_bytes(const la_gated_shape* shape, int backward) {
+  GatedProblem p;
+  if (make_gated(shape, backward != 0, p) != LA_OK) return 0;
+  const size_t n = gated_need(p, backward != 0);
+  return n == 0 ? 256 : n;
+}
+
+la_status la_gated_attention(const la_gated_shape* shape, const void* Q, const void* K,
+                             const void* V, const float* G, const float* S_in, float* S_out,
+                             void* O, void* ws, size_t ws_bytes, la_stream stream) {
+  GatedProblem p;
+  LA_TRY(make_gated(shape, false, p));
+  const bool any_state = p.B > 0 && p.H > 0, any = any_state && p.N > 0;
+  LA_TRY(check_ptr(Q, "Q", any));
+  LA_TRY(check_ptr(K, "K", any));
+  LA_TRY(check_ptr(V, "V", any));
+  LA_TRY(check_ptr(G, "G", any));
+  LA_TRY(check_ptr(O, "O", any));
+  LA_TRY(check_ptr(S_in, "S_in", any_state && S_in != nullptr));
+  LA_TRY(check_ptr(S_out, "S_out", any_state && S_out != nullptr));
+  const size_t need = gated_need(p, false);
+  LA_TRY(check_workspace(ws, ws_bytes, need));
+  const size_t rows = static_cast<size_t>(p.B) * p.N * p.H;
+  const size_t nx = rows * kD * (p.io == LA_IO_BF16 ? 2 : 4), ng = rows * 4;
+  const size_t ns = static_cast<size_t>(p.B) * p.H * kD * kD * 4;
+  const Buffer ins[] = {{Q, nx, "Q"}, {K, nx, "K"}, {V, nx, "V"}, {G, ng, "G"}, {ws, need, "the workspace"},
+                        {S_in == S_out ? nullptr : S_in, ns, "S_in"}};
+  const Buffer outs[] = {{O, nx, "O"}, {S_out, ns, "S_out"}};
+  LA_TRY(check_apart(outs, ins));
+  if (overlap(ws, need, S_in, ns))
+    return fail(LA_ERR_INVALID_ARG, "S_in and the workspace overlap");
+  if (!any_state) return LA_OK;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (!any) return pass_on(S_out, S_in, ns, st);
+  const cudaError_t e =
+      launch_gated(p, Q, K, V, G, S_in, S_out, O, static_cast<float*>(ws), st);
+  if (e != cudaSuccess) return cuda_fail(e, "gated attention");
+  return LA_OK;
+}
+
+la_status la_gated_attention_backward(const la_gated_shape* shape, const void* Q, const void* K,
+                                      const void* V, const float* G, const float* S_in,
+                                      const void* dO, const float* dS_out, void* dQ, void* dK,
+                                      void* dV, float* dG, float* dS_in, void* ws,
+                                      size_t ws_bytes, la_stream stream) {
+  GatedProblem p;
+  LA_TRY(make_gated(shape, true, p));
+  const bool any_state = p.B > 0 && p.H > 0, any = any_state && p.N > 0;
+  LA_TRY(check_ptr(Q, "Q", any));
+  LA_TRY(check_ptr(K, "K", any));
+  LA_TRY(check_ptr(V, "V", any));
+  LA_TRY(check_ptr(G, "G", any));
+  LA_TRY(check_ptr(dO, "dO", any));
+  LA_TRY(check_ptr(dQ, "dQ", any));
+  LA_TRY(check_ptr(dK, "dK", any));
+  LA_TRY(check_ptr(dV, "dV", any));
+  LA_TRY(check_ptr(dG, "dG", any));
+  LA_TRY(check_ptr(S_in, "S_in", any_state && S_in != nullptr));
+  LA_TRY(check_ptr(dS_out, "dS_out", any_state && dS_out != nullptr));
+  LA_TRY(check_ptr(dS_in, "dS_in", any_state && dS_in != nullptr));
+  const size_t need = gated_need(p, true);
+  LA_TRY(check_workspace(ws, ws_bytes, need));
+  const size_t rows = static_cast<size_t>(p.B) * p.N * p.H;
+  const size_t nx = rows * kD * (p.io == LA_IO_BF16 ? 2 : 4), ng = rows * 4;
+  const size_t ns = static_cast<size_t>(p.B) * p.H * kD * kD * 4;
+  const Buffer ins[] = {{Q, nx, "Q"}, {K, nx, "K"}, {V, nx, "V"}, {G, ng, "G"},
+                        {S_in, ns, "S_in"}, {dO, nx, "dO"}, {dS_out, ns, "dS_out"}};
+  const Buffer outs[] = {{dQ, nx, "dQ"}, {dK, nx, "dK"}, {dV, nx, "dV"}, {dG, ng, "dG"},
+                         {dS_in, ns, "dS_in"}, {ws, need, "the workspace"}};
+  LA_TRY(check_apart(outs, ins));
+  if (!any_state) return LA_OK;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (!any) return pass_on(dS_in, dS_out, ns, st);
+  const cudaError_t e = launch_gated_backward(p, Q, K, V, G, S_in, dO, dS_out, dQ, dK, dV, dG,
+                                              dS_in, static_cast<float*>(ws), st);
+  if (e != cudaSuccess) return cuda_fail(e, "gated attention backward");
+  return LA_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,35 @@
+// Internal interface between the C-ABI layer of the block operators
+// (la_block_api.cu) and their kernels: gated linear attention, rotary
+// positions, the gated residual with the norms around it.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+
+#include "la.h"
+
+namespace la {
+
+// Gated linear attention (la_gated.cu, la_gated_backward.cu).
+struct GatedProblem {
+  int B, N, H;
+  int io;       // 0 bf16, 1 float32
+  float scale;  // applied to the queries
+  int seg;      // tokens of one warp's segment, a multiple of 16
+  int nseg;     // segments per (batch element, head)
+};
+constexpr int kGateBlock = 16;      // tokens of one tensor-core block
+constexpr int kGateStepTokens = 8;  // up to here tokens are walked one by one
+constexpr int kGateAnchor = 256;    // tokens between two stored states of the backward
+
+void gated_split(GatedProblem& p, bool backward);
+size_t gated_workspace_floats(const GatedProblem& p, bool backward);
+cudaError_t launch_gated(const GatedProblem& p, const void* Q, const void* K, const void* V,
+                         const float* G, const float* S_in, float* S_out, void* O, float* ws,
+                         cudaStream_t s);
+cudaError_t launch_gated_backward(const GatedProblem& p, const void* Q, const void* K,
+                                  const void* V, const float* G, const float* S_in,
+                                  const void* dO, const float* dS_out, void* dQ, void* dK,
+                                  void* dV, float* dG, float* dS_in, float* ws, cudaStream_t s);
+
+}  // namespace la

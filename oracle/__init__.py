@@ -31,3 +31,9 @@ from .linear_attention import (  # noqa: F401
 )
 from .temporal_conv import temporal_conv  # noqa: F401,E402
 from .qkv_state import bf16_round, qkv_projection, qkv_state, key_value_heads  # noqa: F401,E402
+from .gated import (  # noqa: F401,E402
+    gated_attention,
+    gated_attention_backward,
+    gated_bruteforce,
+    gated_magnitudes,
+)

@@ -1,0 +1,239 @@
+"""GPU parity of gated linear attention against the float64 oracle, element by element.
+
+Tolerances. Every output is a sum of products; with A the sum of the absolute values of
+its terms, |got - ref| <= half a step of the output's type x |ref| + tol x A. For bf16
+tensors the computed operands enter the products as two bf16 parts (2^-17 each; a term
+meets three: decayed key, state, and on its way the state's own, so 2^-15), for float32
+as three (24 bits, sums of up to 32 + 16 terms a product in float32, 2^-18). Each block of
+16 tokens a term has crossed adds the error of one decay, 2^-22.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle as orc
+from tests import parity as P
+
+la = P.la
+pytestmark = pytest.mark.gpu
+D = 32
+HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
+
+
+def _tol(io, N):
+    return (2.0 ** -15 if io == "bf16" else 2.0 ** -18) + -(-N // 16) * 2.0 ** -22
+
+
+def _draw(B, N, H, io, seed, gates="mixed", carry=True):
+    r = torch.Generator().manual_seed(seed)
+    dt = torch.bfloat16 if io == "bf16" else torch.float32
+    q, k, v, do = (torch.randn((B, N, H, D), generator=r).to(dt) for _ in range(4))
+    u = torch.rand((B, N, H), generator=r)
+    rate = 0.002 * 250.0 ** torch.rand((H,), generator=r)
+    g = -rate * (0.1 + 2 * u)
+    if gates == "open":
+        g = torch.zeros_like(g)
+    elif gates == "strong":
+        g = -100.0 * u
+    elif gates == "stops":            # single stops, pairs, whole blocks of them
+        g = torch.where(u < 0.15, torch.full_like(g, -float("inf")), g)
+        g[:, 20:41] = -float("inf")
+        g[:, 0] = -1e30
+    elif gates == "shut":
+        g = torch.full_like(g, -float("inf"))
+    S, dS = (torch.randn((B, H, D, D), generator=r) if carry else None for _ in range(2))
+    return q, k, v, g, do, S, dS
+
+
+def _dev(*xs):
+    return [None if x is None else x.contiguous().cuda() for x in xs]
+
+
+def _check(name, got, ref, mag, tol, half):
+    got = orc.to_f64(got.cpu())
+    err, bound = np.abs(got - ref), half * np.abs(ref) + tol * mag + 1e-36
+    worst = (err / bound).max() if err.size else 0.0
+    assert np.isfinite(got).all() and (err <= bound).all(), f"{name}: {worst:.3g} of its bound"
+
+
+def _forward(case, io, gates, carry, seed=5, scale=0.3):
+    B, N, H = case
+    q, k, v, g, _, S, _ = _draw(B, N, H, io, seed, gates, carry)
+    O, So = la.gated_attention(*_dev(q, k, v, g), S_in=_dev(S)[0], scale=scale, want_state=True)
+    O_ref, S_ref = orc.gated_attention(q, k, v, g, S, scale)
+    A, AS = orc.gated_magnitudes(q, k, v, g, S_in=S, scale=scale)
+    tol = _tol(io, N)
+    _check("O", O, O_ref, A, tol, HALF[io])
+    _check("S", So, S_ref, AS, tol, HALF["f32"])
+
+
+LENGTHS = [1, 2, 8, 9, 15, 16, 17, 33, 63, 64, 65, 127, 200, 517]
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("N", LENGTHS)
+def test_forward_lengths(cuda_device, io, N):
+    _forward((2, N, 3), io, "mixed", N % 2 == 1)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("gates", ["open", "strong", "stops", "shut"])
+@pytest.mark.parametrize("N", [7, 150])
+def test_forward_gates(cuda_device, io, gates, N):
+    _forward((1, N, 5), io, gates, True)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("case", [(20, 70, 130), (1, 3000, 2), (3, 1, 500), (1, 100, 1), (5, 700, 9)],
+                         ids=str)
+def test_forward_shapes(cuda_device, io, case):
+    """One segment per head (more heads than warps fit), many segments, odd counts."""
+    _forward(case, io, "mixed", True)
+
+
+def _backward(case, io, gates, carry, seed=9, scale=0.4):
+    B, N, H = case
+    q, k, v, g, do, S, dS = _draw(B, N, H, io, seed, gates, carry)
+    dq, dk, dv, dg, dso = _dev(q, k, v, g, do)
+    Sd, dSd = _dev(S, dS)
+    got = la.gated_attention_backward(dq, dk, dv, dg, dso, S_in=Sd, dS_out=dSd, scale=scale)
+    ref = orc.gated_attention_backward(q, k, v, g, do, S, dS, scale)
+    mag = orc.gated_magnitudes(q, k, v, g, do, S, dS, scale)
+    names = ("dQ", "dK", "dV", "dG", "dS_in")
+    for i, name in enumerate(names):
+        if got[i] is None:
+            assert name == "dS_in" and not carry
+            continue
+        half = HALF[io] if i < 3 else HALF["f32"]
+        _check(name, got[i], ref[i], mag[i], _tol(io, N) * (2 if name == "dG" else 1), half)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("N", LENGTHS)
+def test_backward_lengths(cuda_device, io, N):
+    _backward((2, N, 3), io, "mixed", N % 2 == 1)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("gates", ["open", "strong", "stops", "shut"])
+@pytest.mark.parametrize("N", [7, 150])
+def test_backward_gates(cuda_device, io, gates, N):
+    _backward((1, N, 5), io, gates, True)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("case", [(20, 70, 130), (1, 3000, 2), (7, 300, 259), (5, 700, 9)], ids=str)
+def test_backward_shapes(cuda_device, io, case):
+    _backward(case, io, "mixed", case[0] != 5)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_gradients_equal_differences(cuda_device, io):
+    """Directional differences of the forward's own outputs, in float32 tensors of the
+    same inputs: the loss moves by the gradient's product with the direction. The step
+    of 2^-6 leaves a quadratic term, cancelled by the two sides, and a cubic one (the
+    gates' exponentials) far below the bound."""
+    q, k, v, g, do, S, dS = _draw(2, 90, 3, io, 21)
+    dev = _dev(q, k, v, g, do, S, dS)
+    grads = la.gated_attention_backward(*dev[:5], S_in=dev[5], dS_out=dev[6])
+    r = torch.Generator().manual_seed(3)
+    ins = [x.double() for x in (q, k, v, g, S)]
+
+    def loss(xs):
+        f = _dev(*[x.float() for x in xs])
+        O, So = la.gated_attention(*f[:4], S_in=f[4], want_state=True)
+        return float((O.double().cpu() * do.double()).sum() + (So.double().cpu() * dS.double()).sum())
+
+    h = 2.0 ** -6
+    for i in range(5):
+        way = torch.randn(ins[i].shape, generator=r, dtype=torch.float64)
+        lo, hi = list(ins), list(ins)
+        lo[i], hi[i] = ins[i] - h * way, ins[i] + h * way
+        step = (loss(hi) - loss(lo)) / (2 * h)
+        want = float((grads[i].double().cpu() * way).sum())
+        size = float((grads[i].double().cpu() * way).norm())
+        assert abs(step - want) <= 2e-2 * size + 1e-3, (i, step, want, size)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("cuts", [(300, 1, 1, 5, 40), (8, 9, 330)], ids=str)
+def test_pieces_equal_the_whole(cuda_device, io, cuts):
+    """Prompt, then single tokens, the state updated in place: the oracle's outputs of
+    the whole sequence."""
+    B, N, H = 2, sum(cuts), 4
+    q, k, v, g, _, S, _ = _draw(B, N, H, io, 33)
+    state, outs, n = S.cuda(), [], 0
+    for c in cuts:
+        part = _dev(*(x[:, n:n + c] for x in (q, k, v, g)))
+        O, same = la.gated_attention(*part, S_in=state, S_out=state)
+        assert same is state
+        outs.append(O)
+        n += c
+    O_ref, S_ref = orc.gated_attention(q, k, v, g, S)
+    A, AS = orc.gated_magnitudes(q, k, v, g, S_in=S)
+    _check("O", torch.cat(outs, 1), O_ref, A, _tol(io, N), HALF[io])
+    _check("S", state, S_ref, AS, _tol(io, N), HALF["f32"])
+
+
+def test_state_in_place_with_segments(cuda_device):
+    q, k, v, g, _, S, _ = _draw(1, 2000, 3, "bf16", 4)
+    dev = _dev(q, k, v, g)
+    state = S.cuda()
+    O1, S1 = la.gated_attention(*dev, S_in=state, want_state=True)
+    O2, S2 = la.gated_attention(*dev, S_in=state, S_out=state)
+    assert S2 is state and torch.equal(O1, O2) and torch.equal(S1, S2)
+
+
+def test_empty_sequence_passes_the_state_on(cuda_device):
+    e = torch.empty((2, 0, 3, D), dtype=torch.bfloat16, device="cuda")
+    g = torch.empty((2, 0, 3), device="cuda")
+    S = torch.randn((2, 3, D, D), device="cuda")
+    O, So = la.gated_attention(e, e, e, g, S_in=S, want_state=True)
+    assert O.shape == e.shape and torch.equal(So, S)
+    assert not la.gated_attention(e, e, e, g, want_state=True)[1].any()
+    *_, dS = la.gated_attention_backward(e, e, e, g, e, S_in=S, dS_out=S)
+    assert torch.equal(dS, S)
+
+
+def test_same_bits_on_any_stream_and_in_a_graph(cuda_device):
+    q, k, v, g, do, S, dS = _dev(*_draw(2, 700, 5, "bf16", 8))
+    fwd = lambda: la.gated_attention(q, k, v, g, S_in=S, want_state=True)  # noqa: E731
+    bwd = lambda: la.gated_attention_backward(q, k, v, g, do, S_in=S, dS_out=dS)  # noqa: E731
+    want = [*fwd(), *bwd()]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = [*fwd(), *bwd()]
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = [*fwd(), *bwd()]
+    keep = q.clone()
+    q.mul_(2.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert not torch.equal(held[0], want[0])
+    q.copy_(keep)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, held))
+
+
+def test_later_tokens_and_other_rows_do_not_reach_earlier_ones(cuda_device):
+    q, k, v, g, *_ = _draw(2, 100, 2, "bf16", 12)
+    O1 = la.gated_attention(*_dev(q, k, v, g))
+    k2, v2, g2 = k.clone(), v.clone(), g.clone()
+    k2[:, 51:], v2[:, 51:], g2[:, 51:] = 3.0, -2.0, -0.01
+    O2 = la.gated_attention(*_dev(q, k2, v2, g2))
+    assert torch.equal(O1[:, :51], O2[:, :51]) and not torch.equal(O1[:, 51:], O2[:, 51:])
+    # what follows the last token in memory stays as it was
+    B, N, H = 1, 37, 2
+    buf = torch.full((B * N * H * D + 4096,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = buf[:B * N * H * D].view(B, N, H, D)
+    dev = _dev(*(x[:1, :N].contiguous() for x in (q, k, v, g)))
+    shape = la.make_gated_shape(B, N, H)
+    ws = torch.empty(la.la_gated_workspace_bytes(shape), dtype=torch.uint8, device="cuda")
+    la.la_gated_attention(shape, *dev, None, None, out, ws)
+    assert torch.equal(out, la.gated_attention(*dev)) and bool((buf[B * N * H * D:] == 7.0).all())
