@@ -35,6 +35,11 @@ namespace {
 
 constexpr int kWarps = 4;  // warps of a CTA: neighbouring heads of one segment
 
+template <bool k>
+struct Const {
+  static constexpr bool value = k;
+};
+
 struct Walk {
   const void *q, *k, *v, *w;  // operands; w: one more tile (see each kernel)
   const float* G;
@@ -42,321 +47,397 @@ struct Walk {
   const float* init;     // external state at the walk's start, [B*H][32*32], or null
   float* final_;         // external state at the walk's end, or null
   const float* prefix;   // state at the start of each segment (nseg > 1), [B*H][nseg][1024]
-  float* anchors;        // backward: S every kGateAnchor tokens, [B*H][anchors][1024]
+  float* anchors;        // backward: S every `anchor` tokens of a segment and at the row's
+                         // end, [B*H][nseg * per_seg + 1][1024]
   float* rows;           // backward: q . dq of every token, [B*H][N]
   float* dG;
-  int anchor, nanchor;   // tokens between anchors; anchors per head
+  int anchor, per_seg;   // tokens between anchors; anchors of a segment
   GatedProblem p;
 };
 
-__device__ __forceinline__ size_t head_base(const GatedProblem& p, int bh) {
-  return (static_cast<size_t>(bh / p.H) * p.N * p.H + bh % p.H) * 32;
+// A warp's place: head bh, tokens [n_begin, n_end), walked in `iters` steps of 16 NB.
+template <int NB>
+struct Place {
+  int bh, seg, n_begin, n_end, iters;
+  size_t stride, base, gbase;
+  __device__ __forceinline__ Place(const GatedProblem& p, long long unit) {
+    const int BH = p.B * p.H;
+    seg = static_cast<int>(unit / BH);
+    bh = static_cast<int>(unit % BH);
+    n_begin = seg * p.seg;
+    n_end = min(p.N, n_begin + p.seg);
+    iters = (n_end - n_begin + NB * kGateBlock - 1) / (NB * kGateBlock);
+    stride = static_cast<size_t>(p.H) * 32;
+    gbase = static_cast<size_t>(bh / p.H) * p.N * p.H + bh % p.H;
+    base = gbase * 32;
+  }
+};
+
+// The lane's piece of an output's next block.
+template <int NP>
+struct Out {
+  char* p;
+  ptrdiff_t down, block;  // bytes to the lane's next piece, to the next block
+  __device__ __forceinline__ Out(void* o, size_t base, size_t stride, int n0, int lane) {
+    using T = typename Io<NP>::T;
+    constexpr int kChunks = NP == 1 ? 4 : 8;
+    p = reinterpret_cast<char*>(static_cast<T*>(o) + base + (n0 + lane / kChunks) * stride) +
+        (lane % kChunks) * 16;
+    down = static_cast<ptrdiff_t>(TileLane<NP>::kRows * stride * sizeof(T));
+    block = static_cast<ptrdiff_t>(kGateBlock * stride * sizeof(T));
+  }
+};
+
+// Two bf16 blocks a step share one split of the state and one update, and fill the 32 lanes
+// with gates; float32 planes would not fit twice in shared memory beside enough warps.
+template <int NP>
+constexpr int kBlocks = NP == 1 ? 2 : 1;
+// Parts of what the kernels compute: two for a bf16 output, three for what ends in float32
+// (the gate's gradient is a difference of row sums) and for float32 tensors. The state's own
+// update always keeps 24 bits.
+constexpr __host__ __device__ int parts(int NP, bool precise) { return NP == 1 && !precise ? 2 : 3; }
+
+// Products of one block row (16 tokens) with the tiles of its step, decayed and summed onto
+// `acc`. kLater: the row's tokens are the later ones of each pair (forward), else the earlier
+// ones (backward). rowf: the row block's operand; colt / deept: shared-memory tiles whose
+// tokens are the columns, and the depth of the second product.
+template <int NP, int NB, int NC, bool kLater, bool kHard>
+__device__ __forceinline__ void block_row(float (&acc)[4][4], int b, const Frag<NP>& rowf,
+                                          uint32_t colt, uint32_t deept, int plane,
+                                          const LaneOff& off, const Decay<NP, NB>& d, float head,
+                                          float tail, float scale, int lane) {
+#pragma unroll
+  for (int o = 0; o < NB; ++o) {  // the other block
+    if (kLater ? o > b : o < b) continue;
+    float w[2][4];
+    {
+      Frag<NP> c;
+      c.cols(colt + o * kPlane, plane, off);
+      token_product(w, rowf, c);
+    }
+    float l[2][4];
+    if (o == b) {
+      d.template within<kLater, kHard>(b, lane, l);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) l[h][x] *= scale;
+    } else {
+      float r[2], c[4];
+      Decay<NP, NB>::spread_rows((kLater ? head : tail) * scale, b, lane, r);
+      Decay<NP, NB>::spread(kLater ? tail : head, o, lane, c);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) l[h][x] = r[h] * c[x];
+    }
+    decay_by<kHard>(w, l);
+    Frag<NP> v;
+    v.deep(deept + o * kPlane, plane, off);
+    if (o == b)
+      weigh<NP, NC, kLater ? 2 : 1>(acc, w, v);
+    else
+      weigh<NP, NC, -1>(acc, w, v);
+  }
 }
 
 // One segment forwards. kBack = false: the forward itself, state rows = v's
 // dimensions. kBack = true: dq from (q, k, v) = (dO, V, K) with w = Q; it also
 // writes q . dq of every token and S at the anchors.
 template <int NP, bool kBack, int kStages>
-__global__ void __launch_bounds__(kWarps * 32, (kBack || NP == 3) ? 3 : 4)
-walk_kernel(const Walk a) {
+__global__ void __launch_bounds__(kWarps * 32, 3) walk_kernel(const Walk a) {
   using T = typename Io<NP>::T;
-  constexpr int NC = NP == 1 ? 2 : 3;
-  constexpr int NT = kBack ? 4 : 3;
-  using M = Smem<NP, NT, kStages, 3>;
+  constexpr int NB = kBlocks<NP>, NT = kBack ? 4 : 3, NC = parts(NP, kBack);
+  constexpr int kStep = NB * kGateBlock;
+  using M = Smem<NP, NB, NT, kStages, 3>;
   extern __shared__ __align__(128) uint8_t smem_all[];
   const GatedProblem& p = a.p;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long unit = static_cast<long long>(blockIdx.x) * kWarps + warp;
-  const int BH = p.B * p.H;
-  if (unit >= static_cast<long long>(BH) * p.nseg) return;
-  const int seg = static_cast<int>(unit / BH), bh = static_cast<int>(unit % BH);
-  const int n_begin = seg * p.seg, n_end = min(p.N, n_begin + p.seg);
-  const int nblk = (n_end - n_begin + kGateBlock - 1) / kGateBlock;
-  const size_t stride = static_cast<size_t>(p.H) * 32;
-  const size_t base = head_base(p, bh);
-  const T* src[4] = {static_cast<const T*>(a.q) + base, static_cast<const T*>(a.k) + base,
-                     static_cast<const T*>(a.v) + base,
-                     kBack ? static_cast<const T*>(a.w) + base : nullptr};
-  const float* G = a.G + static_cast<size_t>(bh / p.H) * p.N * p.H + bh % p.H;
-  uint8_t* smem = smem_all + warp * M::kWarp;
-  uint8_t* planes = smem + kStages * M::kStage;
-  const uint32_t smem_u = smem_addr(smem);
-
-  auto issue = [&](int blk) {
-    if (blk < nblk) {
-      const uint32_t st = smem_u + (blk % kStages) * M::kStage;
-      const int n0 = n_begin + blk * kGateBlock;
+  if (unit >= static_cast<long long>(p.B) * p.H * p.nseg) return;
+  const Place<NB> at(p, unit);
+  const T* heads[NT];
+  heads[0] = static_cast<const T*>(a.q) + at.base;
+  heads[1] = static_cast<const T*>(a.k) + at.base;
+  heads[2] = static_cast<const T*>(a.v) + at.base;
+  if (kBack) heads[NT - 1] = static_cast<const T*>(a.w) + at.base;
+  const uint32_t smem = smem_addr(smem_all) + warp * M::kWarp;
+  const uint32_t planes = smem + kStages * M::kStage;
+  Ring<NP, NB, NT, kStages, 3, false, false> ring(smem, heads, a.G + at.gbase, p.H, nullptr,
+                                                  at.n_begin, at.n_end, at.iters, lane);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) load_tile<NP>(st + t * M::kTile, src[t], stride, n0, n_end, lane);
-      if (lane < 16) {
-        const bool in = n0 + lane < n_end;
-        cp4(st + NT * M::kTile + lane * 4, G + (in ? static_cast<size_t>(n0 + lane) * p.H : 0),
-            in ? 4 : 0);
-      }
-    }
-    cp_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue(i);
+  for (int i = 0; i < kStages - 1; ++i) ring.issue(lane);
+  const TileLane<NP> tl(lane);
+  Out<NP> out(a.o, at.base, at.stride, at.n_begin, lane);
 
   State S;
   if (p.nseg > 1)
-    S.load(a.prefix + (static_cast<size_t>(bh) * p.nseg + seg) * 1024, lane);
+    S.load(a.prefix + (static_cast<size_t>(at.bh) * p.nseg + at.seg) * 1024, lane);
   else if (a.init != nullptr)
-    S.template load_outer<!kBack>(a.init + static_cast<size_t>(bh) * 1024, lane);
+    S.template load_outer<!kBack>(a.init + static_cast<size_t>(at.bh) * 1024, lane);
   else
     S.zero();
+  float* anchors = nullptr;
+  if (kBack)
+    anchors = a.anchors + (static_cast<size_t>(at.bh) * (p.nseg * a.per_seg + 1) +
+                           static_cast<size_t>(at.seg) * a.per_seg) * 1024;
   const LaneOff off(lane);
   const int r0 = lane >> 2;
 
-  for (int blk = 0; blk < nblk; ++blk) {
-    cp_wait<kStages - 2>();
-    __syncwarp();
-    issue(blk + kStages - 1);  // into the stage that the block before has left
-    uint8_t* st = smem + (blk % kStages) * M::kStage;
-    const int n0 = n_begin + blk * kGateBlock;
-    const float gate = *reinterpret_cast<const float*>(st + NT * M::kTile + (lane & 15) * 4);
+  int n0 = at.n_begin;
+  for (int it = 0; it < at.iters; ++it, n0 += kStep) {
+    const uint32_t st = ring.next(lane);
+    const float gate = lds(st + NT * M::kTile + lane * 4);
     uint32_t tile[3];
+    int plane = 0;
     if (NP == 1) {
 #pragma unroll
-      for (int t = 0; t < 3; ++t) tile[t] = smem_addr(st) + t * M::kTile;
+      for (int t = 0; t < 3; ++t) tile[t] = st + t * M::kTile;
     } else {
+      plane = M::kPart;
 #pragma unroll
       for (int t = 0; t < 3; ++t) {
-        split_tile(st + t * M::kTile, planes + t * 3 * kPlane, lane);
-        tile[t] = smem_addr(planes) + t * 3 * kPlane;
+        split_tile<NB>(st + t * M::kTile, planes + t * 3 * M::kPart, lane);
+        tile[t] = planes + t * 3 * M::kPart;
       }
       __syncwarp();
     }
-    if (kBack && (n0 % a.anchor) == 0)
-      S.store(a.anchors + (static_cast<size_t>(bh) * a.nanchor + n0 / a.anchor) * 1024, lane);
+    if (kBack && (n0 - at.n_begin) % a.anchor == 0)
+      S.store(anchors + static_cast<size_t>((n0 - at.n_begin) / a.anchor) * 1024, lane);
 
-    const Decay d(gate, lane);
-    float acc[4][4];
+    const Decay<NP, NB> d(gate, lane);
+    const float head = d.head(lane), tail = d.tail(lane), whole = d.whole(lane);
+    // decays of the step's blocks, from its start and to its end
+    const float w0 = __shfl_sync(0xffffffffu, whole, 0);
+    const float w1 = NB == 1 ? 1.0f : __shfl_sync(0xffffffffu, whole, 16);
+    const float from_start = (NB == 2 && lane >= 16 ? head * w0 : head) * p.scale;
+    float acc[NB][4][4];
+    Frag<NP> q[NB];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int b = 0; b < NB; ++b) q[b].rows(tile[0] + b * kPlane, plane, off);
+    S.template apply<NP, NC, NB>(acc, q);
+    auto rest = [&](auto hard) {
+      constexpr bool kHard = decltype(hard)::value;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[e][i] = 0.0f;
-    float w[2][4];
+      for (int b = 0; b < NB; ++b) {
+        float r[2];
+        Decay<NP, NB>::spread_rows(from_start, b, lane, r);
+        scale_row<kHard>(acc[b], 0, r[0]);
+        scale_row<kHard>(acc[b], 1, r[1]);
+        block_row<NP, NB, NC, true, kHard>(acc[b], b, q[b], tile[1], tile[2], plane, off, d, head,
+                                           tail, p.scale, lane);
+      }
+    };
+    if (d.hard)
+      rest(Const<true>());
+    else
+      rest(Const<false>());
     {
-      Frag<NP> q, k;
-      q.rows(tile[0], off);
-      k.cols(tile[1], off);
-      token_product(w, q, k);
-      S.template apply<NP, NC>(acc, q);
+      const float to_end = NB == 2 && lane < 16 ? tail * w1 : tail;
+      float wt[NB][4];
+      Frag<NP> v[NB], k[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        Decay<NP, NB>::spread(to_end, b, lane, wt[b]);
+        v[b].deep(tile[2] + b * kPlane, plane, off);
+        k[b].deep(tile[1] + b * kPlane, plane, off);
+      }
+      S.template update<NP, NB>(w0 * w1, v, k, wt);
     }
-    {
-      const float head = d.head(lane) * p.scale;
-      float l[2][4];
-      d.between<true>(lane, l);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        scale_row(acc, h, __shfl_sync(0xffffffffu, head, r0 + 8 * h));
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          float& e = w[x >> 1][2 * h + (x & 1)];
-          e = l[h][x] == 0.0f ? 0.0f : e * (l[h][x] * p.scale);
+    for (int b = 0; b < NB; ++b) {
+      const int left = at.n_end - n0 - b * kGateBlock;
+      if (kBack) {
+        float dots[2];
+        row_dots<NP>(acc[b], st + 3 * M::kTile + b * M::kTile / NB, tl, dots);
+        if ((lane & 3) == 0) {
+          float* r = a.rows + static_cast<size_t>(at.bh) * p.N + n0 + b * kGateBlock + r0;
+          if (r0 < left) r[0] = dots[0];
+          if (r0 + 8 < left) r[8] = dots[1];
         }
       }
+      __syncwarp();  // every lane is done with the first tile: the output passes through it
+      store_tile<NP>(acc[b], st + b * M::kTile / NB, tl, out.p + b * out.block, out.down, left, lane);
     }
-    Frag<NP> v;
-    v.deep(tile[2], off);
-    weigh<NP, NC>(acc, w, v);
-    {
-      float wt[4];
-      Decay::spread(d.tail(lane), lane, wt);
-      Frag<NP> k;
-      k.deep(tile[1], off);
-      S.template update<NP, NC>(d.whole(), v, k, wt);
-    }
-    if (kBack) {
-      float dots[2];
-      row_dots<NP>(acc, st + 3 * M::kTile, lane, dots);
-      if ((lane & 3) == 0) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (n0 + r0 + 8 * h < n_end)
-            a.rows[static_cast<size_t>(bh) * p.N + n0 + r0 + 8 * h] = dots[h];
-      }
-    }
-    __syncwarp();  // every lane is done with the first tile: the output passes through it
-    store_tile<NP>(acc, st, static_cast<T*>(a.o) + base, stride, n0, n_end, lane);
+    out.p += NB * out.block;
   }
   cp_wait<0>();
-  if (seg == p.nseg - 1) {
+  if (at.seg == p.nseg - 1) {
     if (!kBack && a.final_ != nullptr)
-      S.template store_outer<true>(a.final_ + static_cast<size_t>(bh) * 1024, lane);
-    if (kBack)  // the state after the last token: the anchor of the sequence's end
-      S.store(a.anchors + (static_cast<size_t>(bh) * a.nanchor + a.nanchor - 1) * 1024, lane);
+      S.template store_outer<true>(a.final_ + static_cast<size_t>(at.bh) * 1024, lane);
+    if (kBack)  // the state after the last token: the anchor of the row's end
+      S.store(anchors + static_cast<size_t>(a.per_seg) * 1024, lane);
   }
 }
 
 // One segment backwards: dk and dv (o and o2), the log gates' gradient, and with
 // a.final_ the gradient of the state before the first token. q, k, v as in the
 // forward, w = dO. The carried state X (rows: k's dimensions, columns: v's) is the
-// gradient that reaches the state at a block's end from later tokens.
+// gradient that reaches the state at a step's end from later tokens.
 template <int NP, int kStages>
 __global__ void __launch_bounds__(kWarps * 32, NP == 3 ? 2 : 3) walk_back_kernel(const Walk a) {
   using T = typename Io<NP>::T;
-  constexpr int NC = NP == 1 ? 2 : 3;
-  constexpr int NT = 4;
-  using M = Smem<NP, NT, kStages>;
+  constexpr int NB = kBlocks<NP>, NT = 4, NK = parts(NP, true), NV = parts(NP, false);
+  constexpr int kStep = NB * kGateBlock;
+  using M = Smem<NP, NB, NT, kStages>;
   extern __shared__ __align__(128) uint8_t smem_all[];
   const GatedProblem& p = a.p;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long unit = static_cast<long long>(blockIdx.x) * kWarps + warp;
-  const int BH = p.B * p.H;
-  if (unit >= static_cast<long long>(BH) * p.nseg) return;
-  const int seg = static_cast<int>(unit / BH), bh = static_cast<int>(unit % BH);
-  const int n_begin = seg * p.seg, n_end = min(p.N, n_begin + p.seg);
-  const int nblk = (n_end - n_begin + kGateBlock - 1) / kGateBlock;
-  const size_t stride = static_cast<size_t>(p.H) * 32;
-  const size_t base = head_base(p, bh);
-  const T* src[4] = {static_cast<const T*>(a.k) + base, static_cast<const T*>(a.v) + base,
-                     static_cast<const T*>(a.q) + base, static_cast<const T*>(a.w) + base};
-  const size_t gbase = static_cast<size_t>(bh / p.H) * p.N * p.H + bh % p.H;
-  const float* rows = a.rows + static_cast<size_t>(bh) * p.N;
-  uint8_t* smem = smem_all + warp * M::kWarp;
-  uint8_t* planes = smem + kStages * M::kStage;
-  const uint32_t smem_u = smem_addr(smem);
-
-  auto issue = [&](int it) {  // it counts from the segment's last block
-    if (it < nblk) {
-      const uint32_t st = smem_u + (it % kStages) * M::kStage;
-      const int n0 = n_begin + (nblk - 1 - it) * kGateBlock;
+  if (unit >= static_cast<long long>(p.B) * p.H * p.nseg) return;
+  const Place<NB> at(p, unit);
+  const T* const heads[NT] = {static_cast<const T*>(a.k) + at.base, static_cast<const T*>(a.v) + at.base,
+                              static_cast<const T*>(a.q) + at.base, static_cast<const T*>(a.w) + at.base};
+  const uint32_t smem = smem_addr(smem_all) + warp * M::kWarp;
+  const uint32_t planes = smem + kStages * M::kStage;
+  int n0 = at.n_begin + (at.iters - 1) * kStep;  // the last step comes first
+  Ring<NP, NB, NT, kStages, NT, true, true> ring(smem, heads, a.G + at.gbase, p.H,
+                                                 a.rows + static_cast<size_t>(at.bh) * p.N, n0,
+                                                 at.n_end, at.iters, lane);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) load_tile<NP>(st + t * M::kTile, src[t], stride, n0, n_end, lane);
-      const int i = lane & 15;
-      const bool in = n0 + i < n_end;
-      cp4(st + NT * M::kTile + lane * 4,
-          lane < 16 ? a.G + gbase + (in ? static_cast<size_t>(n0 + i) * p.H : 0)
-                    : rows + (in ? n0 + i : 0),
-          in ? 4 : 0);
-    }
-    cp_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue(i);
+  for (int i = 0; i < kStages - 1; ++i) ring.issue(lane);
+  const TileLane<NP> tl(lane);
+  Out<NP> out_k(a.o, at.base, at.stride, n0, lane), out_v(a.o2, at.base, at.stride, n0, lane);
 
   State X;
   if (p.nseg > 1)
-    X.load(a.prefix + (static_cast<size_t>(bh) * p.nseg + seg) * 1024, lane);
+    X.load(a.prefix + (static_cast<size_t>(at.bh) * p.nseg + at.seg) * 1024, lane);
   else if (a.init != nullptr)
-    X.template load_outer<false>(a.init + static_cast<size_t>(bh) * 1024, lane);
+    X.template load_outer<false>(a.init + static_cast<size_t>(at.bh) * 1024, lane);
   else
     X.zero();
-  // dg just past the segment: <X, S> there. At the sequence's end S is the last anchor.
-  const float* anchors = a.anchors + static_cast<size_t>(bh) * a.nanchor * 1024;
+  // dg just past the segment: <X, S> there, S the first anchor of the next one (or the row's
+  // end). Then `carry` is dg of the token after the step at hand.
+  const float* anchors = a.anchors + (static_cast<size_t>(at.bh) * (p.nseg * a.per_seg + 1) +
+                                      static_cast<size_t>(at.seg) * a.per_seg) * 1024;
   float carry;
   {
     State S;
-    S.load(anchors + static_cast<size_t>(seg == p.nseg - 1 ? a.nanchor - 1 : n_end / a.anchor) *
-                         1024, lane);
+    S.load(anchors + static_cast<size_t>(a.per_seg) * 1024, lane);
     carry = X.dot(S);
   }
   const LaneOff off(lane);
-  const int r0 = lane >> 2;
 
-  for (int it = 0; it < nblk; ++it) {
-    cp_wait<kStages - 2>();
-    __syncwarp();
-    issue(it + kStages - 1);
-    uint8_t* st = smem + (it % kStages) * M::kStage;
-    const int n0 = n_begin + (nblk - 1 - it) * kGateBlock;
-    const float gate = *reinterpret_cast<const float*>(st + NT * M::kTile + (lane & 15) * 4);
-    const float rdot = *reinterpret_cast<const float*>(st + NT * M::kTile + 64 + (lane & 15) * 4);
+  for (int it = 0; it < at.iters; ++it, n0 -= kStep) {
+    const uint32_t st = ring.next(lane);
+    const float gate = lds(st + NT * M::kTile + lane * 4);
+    const float rdot = lds(st + NT * M::kTile + 128 + lane * 4);
     uint32_t tile[NT];
+    int plane = 0;
     if (NP == 1) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) tile[t] = smem_addr(st) + t * M::kTile;
+      for (int t = 0; t < NT; ++t) tile[t] = st + t * M::kTile;
     } else {
+      plane = M::kPart;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        split_tile(st + t * M::kTile, planes + t * 3 * kPlane, lane);
-        tile[t] = smem_addr(planes) + t * 3 * kPlane;
+        split_tile<NB>(st + t * M::kTile, planes + t * 3 * M::kPart, lane);
+        tile[t] = planes + t * 3 * M::kPart;
       }
       __syncwarp();
     }
-    const Decay d(gate, lane);
-    float dk[4][4], dv[4][4];
+    const Decay<NP, NB> d(gate, lane);
+    const float head = d.head(lane), tail = d.tail(lane), whole = d.whole(lane);
+    const float w0 = __shfl_sync(0xffffffffu, whole, 0);
+    const float w1 = NB == 1 ? 1.0f : __shfl_sync(0xffffffffu, whole, 16);
+    const float to_end = NB == 2 && lane < 16 ? tail * w1 : tail;
+    float kdots[NB][2];
+    // dk (which = 0): rows v, columns dO, summed over q; dv: rows k, columns q, summed over dO
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
+    for (int which = 0; which < 2; ++which) {
+      float acc[NB][4][4];
+      Frag<NP> x[NB];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dk[e][i] = dv[e][i] = 0.0f;
-    float wk[2][4], wv[2][4];  // rows: token j of k, v; columns: token i of q, dO
-    {
-      Frag<NP> v, k, c;
-      v.rows(tile[1], off);
-      k.rows(tile[0], off);
-      X.template apply_both<NP, NC>(dk, v, dv, k);
-      c.cols(tile[3], off);
-      token_product(wk, v, c);  // v_j . dO_i
-      c.cols(tile[2], off);
-      token_product(wv, k, c);  // k_j . q_i
-    }
-    {
-      const float tail = d.tail(lane);
-      float l[2][4];
-      d.between<false>(lane, l);
+      for (int b = 0; b < NB; ++b) x[b].rows(tile[1 - which] + b * kPlane, plane, off);
+      if (which == 0)
+        X.template apply<NP, NK, NB>(acc, x);
+      else
+        X.template apply_turned<NP, NV, NB>(acc, x);
+      auto rest = [&](auto hard) {
+        constexpr bool kHard = decltype(hard)::value;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float tj = __shfl_sync(0xffffffffu, tail, r0 + 8 * h);
-        scale_row(dk, h, tj);
-        scale_row(dv, h, tj);
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const float f = l[h][x] * p.scale;
-          float& ek = wk[x >> 1][2 * h + (x & 1)];
-          float& ev = wv[x >> 1][2 * h + (x & 1)];
-          ek = l[h][x] == 0.0f ? 0.0f : ek * f;
-          ev = l[h][x] == 0.0f ? 0.0f : ev * f;
+        for (int b = 0; b < NB; ++b) {
+          float r[2];
+          Decay<NP, NB>::spread_rows(to_end, b, lane, r);
+          scale_row<kHard>(acc[b], 0, r[0]);
+          scale_row<kHard>(acc[b], 1, r[1]);
+          if (which == 0)
+            block_row<NP, NB, NK, false, kHard>(acc[b], b, x[b], tile[3], tile[2], plane, off, d,
+                                                head, tail, p.scale, lane);
+          else
+            block_row<NP, NB, NV, false, kHard>(acc[b], b, x[b], tile[2], tile[3], plane, off, d,
+                                                head, tail, p.scale, lane);
         }
-      }
-    }
-    {
-      float wt[4];
-      Decay::spread(d.head(lane) * p.scale, lane, wt);
-      Frag<NP> q, o;
-      q.deep(tile[2], off);
-      o.deep(tile[3], off);
-      weigh<NP, NC>(dk, wk, q);
-      weigh<NP, NC>(dv, wv, o);
-      X.template update<NP, NC>(d.whole(), q, o, wt);
-    }
-    // dg_t = dg_{t+1} + q_t . dq_t - k_t . dk_t, summed from the block's end; a stop
-    // passes no gradient and restarts the sum
-    float dots[2];
-    row_dots<NP>(dk, st, lane, dots);
-    {
-      const int i = lane & 15;
-      const float lo = __shfl_sync(0xffffffffu, dots[0], (i & 7) * 4);
-      const float hi = __shfl_sync(0xffffffffu, dots[1], (i & 7) * 4);
-      float x = rdot - (i < 8 ? lo : hi);
+      };
+      if (d.hard)
+        rest(Const<true>());
+      else
+        rest(Const<false>());
+      if (which == 0) {
+        // k's own tile is still needed: dk waits in the registers of v's, which is not
 #pragma unroll
-      for (int s = 1; s < 16; s <<= 1) {
-        const float y = __shfl_down_sync(0xffffffffu, x, s, 16);
-        if (i + s < 16) x += y;
+        for (int b = 0; b < NB; ++b)
+          row_dots<NP>(acc[b], st + b * M::kTile / NB, tl, kdots[b]);
       }
-      const uint32_t after = d.stops & ~((2u << i) - 1u);
-      const int until = after != 0 ? __ffs(after) - 1 : 0;
-      const float cut = __shfl_sync(0xffffffffu, x, until);
-      float dg = after != 0 ? x - cut : carry + x;
-      if ((d.stops >> i) & 1u) dg = 0.0f;
-      if (lane < 16 && n0 + i < n_end) a.dG[gbase + static_cast<size_t>(n0 + i) * p.H] = dg;
+      __syncwarp();  // v's (then k's) tile has been read: the output passes through it
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+        store_tile<NP>(acc[b], st + (1 - which) * M::kTile + b * M::kTile / NB, tl,
+                       (which == 0 ? out_k : out_v).p + b * out_k.block, out_k.down,
+                       at.n_end - n0 - b * kGateBlock, lane);
+    }
+    out_k.p -= NB * out_k.block;
+    out_v.p -= NB * out_k.block;
+    {
+      const float from_start = (NB == 2 && lane >= 16 ? head * w0 : head) * p.scale;
+      float wt[NB][4];
+      Frag<NP> q[NB], o[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        Decay<NP, NB>::spread(from_start, b, lane, wt[b]);
+        q[b].deep(tile[2] + b * kPlane, plane, off);
+        o[b].deep(tile[3] + b * kPlane, plane, off);
+      }
+      X.template update<NP, NB>(w0 * w1, q, o, wt);
+    }
+    // dg_t = dg_{t+1} + q_t . dq_t - k_t . dk_t, summed from the step's end; a stop
+    // passes no gradient and restarts the sum
+    {
+      const int i = lane & (kStep - 1);
+      float own = 0.0f;
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float y = __shfl_sync(0xffffffffu, kdots[b][h], (i & 7) * 4);
+          if ((i >> 3) == 2 * b + h) own = y;
+        }
+      float x = rdot - own;
+#pragma unroll
+      for (int s = 1; s < kStep; s <<= 1) {
+        const float y = __shfl_down_sync(0xffffffffu, x, s, kStep);
+        if (i + s < kStep) x += y;
+      }
+      float dg = carry + x;
+      if (d.stops != 0) {
+        const uint32_t after = i == 31 ? 0u : d.stops & ~((2u << i) - 1u);
+        const float cut = __shfl_sync(0xffffffffu, x, after != 0 ? __ffs(after) - 1 : 0);
+        if (after != 0) dg = x - cut;
+        if ((d.stops >> i) & 1u) dg = 0.0f;
+      }
+      if (lane < kStep && n0 + i < at.n_end)
+        a.dG[at.gbase + static_cast<size_t>(n0 + i) * p.H] = dg;
       carry = __shfl_sync(0xffffffffu, dg, 0);
     }
-    if (n0 % a.anchor == 0 && n0 > n_begin) {
+    if ((n0 - at.n_begin) % a.anchor == 0 && it + 1 < at.iters) {
       State S;
-      S.load(anchors + static_cast<size_t>(n0 / a.anchor) * 1024, lane);
+      S.load(anchors + static_cast<size_t>((n0 - at.n_begin) / a.anchor) * 1024, lane);
       carry = X.dot(S);
     }
-    __syncwarp();
-    store_tile<NP>(dk, st, static_cast<T*>(a.o) + base, stride, n0, n_end, lane);
-    store_tile<NP>(dv, st + M::kTile, static_cast<T*>(a.o2) + base, stride, n0, n_end, lane);
   }
   cp_wait<0>();
-  if (seg == 0 && a.final_ != nullptr)
-    X.template store_outer<false>(a.final_ + static_cast<size_t>(bh) * 1024, lane);
+  if (at.seg == 0 && a.final_ != nullptr)
+    X.template store_outer<false>(a.final_ + static_cast<size_t>(at.bh) * 1024, lane);
 }
 
 // Every segment's own state from zero and its whole decay. Forward: S only, rows =
@@ -364,105 +445,102 @@ __global__ void __launch_bounds__(kWarps * 32, NP == 3 ? 2 : 3) walk_back_kernel
 // scale q_i^T dO_i, rows = k's (q's) dimensions. Segment s's S goes to slot s + 1 of
 // `states` (it becomes the state at the start of s + 1), its X to slot s - 1 of `grads`.
 template <int NP, bool kBack, int kStages>
-__global__ void __launch_bounds__(kWarps * 32, NP == 3 ? 3 : 4)
+__global__ void __launch_bounds__(kWarps * 32, NP == 1 && !kBack ? 4 : 3)
 segment_kernel(const GatedProblem p, const void* qv, const void* kv, const void* vv,
                const void* dov, const float* Gv, float* states, float* grads, float* decays) {
   using T = typename Io<NP>::T;
-  constexpr int NC = NP == 1 ? 2 : 3;
-  constexpr int NT = kBack ? 4 : 2;
-  using M = Smem<NP, NT, kStages>;
+  constexpr int NB = kBlocks<NP>, NT = kBack ? 4 : 2;
+  constexpr int kStep = NB * kGateBlock;
+  using M = Smem<NP, NB, NT, kStages>;
   extern __shared__ __align__(128) uint8_t smem_all[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long unit = static_cast<long long>(blockIdx.x) * kWarps + warp;
-  const int BH = p.B * p.H;
   const int segs = kBack ? p.nseg : p.nseg - 1;  // nothing follows the last one forwards
-  if (unit >= static_cast<long long>(BH) * segs) return;
-  const int seg = static_cast<int>(unit / BH), bh = static_cast<int>(unit % BH);
-  const int n_begin = seg * p.seg, n_end = min(p.N, n_begin + p.seg);
-  const int nblk = (n_end - n_begin + kGateBlock - 1) / kGateBlock;
-  const size_t stride = static_cast<size_t>(p.H) * 32;
-  const size_t base = head_base(p, bh);
-  const T* src[4] = {static_cast<const T*>(kBack ? kv : vv) + base,
-                     static_cast<const T*>(kBack ? vv : kv) + base,
-                     kBack ? static_cast<const T*>(qv) + base : nullptr,
-                     kBack ? static_cast<const T*>(dov) + base : nullptr};
-  const float* G = Gv + static_cast<size_t>(bh / p.H) * p.N * p.H + bh % p.H;
-  uint8_t* smem = smem_all + warp * M::kWarp;
-  uint8_t* planes = smem + kStages * M::kStage;
-  const uint32_t smem_u = smem_addr(smem);
-  auto issue = [&](int blk) {
-    if (blk < nblk) {
-      const uint32_t st = smem_u + (blk % kStages) * M::kStage;
-      const int n0 = n_begin + blk * kGateBlock;
+  if (unit >= static_cast<long long>(p.B) * p.H * segs) return;
+  const Place<NB> at(p, unit);
+  const T* heads[NT];
+  heads[0] = static_cast<const T*>(kBack ? kv : vv) + at.base;
+  heads[1] = static_cast<const T*>(kBack ? vv : kv) + at.base;
+  if (kBack) {
+    heads[NT - 2] = static_cast<const T*>(qv) + at.base;
+    heads[NT - 1] = static_cast<const T*>(dov) + at.base;
+  }
+  const uint32_t smem = smem_addr(smem_all) + warp * M::kWarp;
+  const uint32_t planes = smem + kStages * M::kStage;
+  Ring<NP, NB, NT, kStages, NT, false, false> ring(smem, heads, Gv + at.gbase, p.H, nullptr,
+                                                   at.n_begin, at.n_end, at.iters, lane);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) load_tile<NP>(st + t * M::kTile, src[t], stride, n0, n_end, lane);
-      if (lane < 16) {
-        const bool in = n0 + lane < n_end;
-        cp4(st + NT * M::kTile + lane * 4, G + (in ? static_cast<size_t>(n0 + lane) * p.H : 0),
-            in ? 4 : 0);
-      }
-    }
-    cp_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) issue(i);
+  for (int i = 0; i < kStages - 1; ++i) ring.issue(lane);
   State S, X;
   S.zero();
   if (kBack) X.zero();
-  float whole = 1.0f;
+  float total = 1.0f;
   const LaneOff off(lane);
-  for (int blk = 0; blk < nblk; ++blk) {
-    cp_wait<kStages - 2>();
-    __syncwarp();
-    issue(blk + kStages - 1);
-    const uint8_t* st = smem + (blk % kStages) * M::kStage;
-    const float gate = *reinterpret_cast<const float*>(st + NT * M::kTile + (lane & 15) * 4);
+  for (int it = 0; it < at.iters; ++it) {
+    const uint32_t st = ring.next(lane);
+    const float gate = lds(st + NT * M::kTile + lane * 4);
     uint32_t tile[NT];
+    int plane = 0;
     if (NP == 1) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t) tile[t] = smem_addr(st) + t * M::kTile;
+      for (int t = 0; t < NT; ++t) tile[t] = st + t * M::kTile;
     } else {
+      plane = M::kPart;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
-        split_tile(st + t * M::kTile, planes + t * 3 * kPlane, lane);
-        tile[t] = smem_addr(planes) + t * 3 * kPlane;
+        split_tile<NB>(st + t * M::kTile, planes + t * 3 * M::kPart, lane);
+        tile[t] = planes + t * 3 * M::kPart;
       }
       __syncwarp();
     }
-    const Decay d(gate, lane);
-    float w[4];
+    const Decay<NP, NB> d(gate, lane);
+    const float whole = d.whole(lane);
+    const float w0 = __shfl_sync(0xffffffffu, whole, 0);
+    const float w1 = NB == 1 ? 1.0f : __shfl_sync(0xffffffffu, whole, 16);
+    float w[NB][4];
     {
-      Decay::spread(d.tail(lane), lane, w);
-      Frag<NP> x, y;
-      x.deep(tile[0], off);
-      y.deep(tile[1], off);
-      S.template update<NP, NC>(d.whole(), x, y, w);
+      const float tail = d.tail(lane);
+      const float to_end = NB == 2 && lane < 16 ? tail * w1 : tail;
+      Frag<NP> x[NB], y[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        Decay<NP, NB>::spread(to_end, b, lane, w[b]);
+        x[b].deep(tile[0] + b * kPlane, plane, off);
+        y[b].deep(tile[1] + b * kPlane, plane, off);
+      }
+      S.template update<NP, NB>(w0 * w1, x, y, w);
     }
     if (kBack) {
-      Decay::spread(d.head(lane) * (p.scale * whole), lane, w);
-      Frag<NP> x, y;
-      x.deep(tile[2], off);
-      y.deep(tile[3], off);
-      X.template update<NP, NC>(1.0f, x, y, w);
+      const float head = d.head(lane);
+      const float from_start =
+          (NB == 2 && lane >= 16 ? head * w0 : head) * (p.scale * total);
+      Frag<NP> x[NB], y[NB];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        Decay<NP, NB>::spread(from_start, b, lane, w[b]);
+        x[b].deep(tile[2] + b * kPlane, plane, off);
+        y[b].deep(tile[3] + b * kPlane, plane, off);
+      }
+      X.template update<NP, NB>(1.0f, x, y, w);
     }
-    whole *= d.whole();
+    total *= w0 * w1;
   }
   cp_wait<0>();
-  const size_t slots = static_cast<size_t>(bh) * p.nseg;
-  if (seg + 1 < p.nseg) S.store(states + (slots + seg + 1) * 1024, lane);
-  if (kBack && seg > 0) X.store(grads + (slots + seg - 1) * 1024, lane);
-  if (lane == 0) decays[slots + seg] = whole;
+  const size_t slots = static_cast<size_t>(at.bh) * p.nseg;
+  if (at.seg + 1 < p.nseg) S.store(states + (slots + at.seg + 1) * 1024, lane);
+  if (kBack && at.seg > 0) X.store(grads + (slots + at.seg - 1) * 1024, lane);
+  if (lane == 0) decays[slots + at.seg] = total;
 }
 
 // Segments in order: slot s becomes the state at segment s's start (forwards), or the
-// gradient at its end (backwards). One thread per four numbers of a head's state;
-// blockIdx.y = 0: states, 1: gradients.
+// gradient at its end (backwards). One thread per four numbers of a head's state, 64 threads
+// a CTA so that few heads still spread over the SMs; blockIdx.z = 0: states, 1: gradients.
 template <bool kTransposed>
-__global__ void __launch_bounds__(256)
-combine_kernel(int BH, int nseg, const float* decays, float* states, const float* s_init,
-               float* grads, const float* x_init) {
-  const int bh = blockIdx.x, f = threadIdx.x;
-  const bool back = blockIdx.y == 1;
+__global__ void __launch_bounds__(64)
+combine_kernel(int nseg, const float* decays, float* states, const float* s_init, float* grads,
+               const float* x_init) {
+  const int bh = blockIdx.x, f = blockIdx.y * 64 + threadIdx.x;
+  const bool back = blockIdx.z == 1;
   float4* slot = reinterpret_cast<float4*>(back ? grads : states) +
                  static_cast<size_t>(bh) * nseg * 256 + f;
   const float* init = back ? x_init : s_init;
@@ -545,8 +623,8 @@ step_kernel(const GatedProblem p, const T* Q, const T* K, const T* V, const floa
   const long long unit = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
   if (unit >= static_cast<long long>(p.B) * p.H) return;
   const int bh = static_cast<int>(unit);
-  const size_t base = head_base(p, bh);
   const size_t gbase = static_cast<size_t>(bh / p.H) * p.N * p.H + bh % p.H;
+  const size_t base = gbase * 32;
   const int e4 = (lane & 7) * 4, dr = lane >> 3;
   float s[8][4];
 #pragma unroll
@@ -599,20 +677,20 @@ template <int NP>
 cudaError_t forward(const GatedProblem& p, const void* Q, const void* K, const void* V,
                     const float* G, const float* S_in, float* S_out, void* O, float* ws,
                     cudaStream_t s) {
-  constexpr int kSegStages = NP == 1 ? 6 : 3, kStages = NP == 1 ? 4 : 2;
+  constexpr int NB = kBlocks<NP>, kSegStages = 3, kStages = NP == 1 ? 3 : 2;
   const long long BH = 1LL * p.B * p.H;
   float* states = ws;
   float* decays = ws + BH * p.nseg * 1024;
   cudaError_t e;
   if (p.nseg > 1) {
     auto seg = segment_kernel<NP, false, kSegStages>;
-    const int bytes = kWarps * Smem<NP, 2, kSegStages>::kWarp;
+    const int bytes = kWarps * Smem<NP, NB, 2, kSegStages>::kWarp;
     if ((e = allow_smem(seg, bytes)) != cudaSuccess) return e;
     seg<<<grid_of(BH * (p.nseg - 1)), kWarps * 32, bytes, s>>>(p, Q, K, V, nullptr, G, states,
                                                               nullptr, decays);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    combine_kernel<true><<<dim3(static_cast<unsigned>(BH), 1), 256, 0, s>>>(
-        static_cast<int>(BH), p.nseg, decays, states, S_in, nullptr, nullptr);
+    combine_kernel<true><<<dim3(static_cast<unsigned>(BH), 4, 1), 64, 0, s>>>(
+        p.nseg, decays, states, S_in, nullptr, nullptr);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   Walk a = {};
@@ -626,36 +704,39 @@ cudaError_t forward(const GatedProblem& p, const void* Q, const void* K, const v
   a.prefix = states;
   a.p = p;
   auto walk = walk_kernel<NP, false, kStages>;
-  const int bytes = kWarps * Smem<NP, 3, kStages, 3>::kWarp;
+  const int bytes = kWarps * Smem<NP, NB, 3, kStages, 3>::kWarp;
   if ((e = allow_smem(walk, bytes)) != cudaSuccess) return e;
   walk<<<grid_of(BH * p.nseg), kWarps * 32, bytes, s>>>(a);
   return cudaGetLastError();
 }
+
+// Anchors of a segment: at its start and every kGateAnchor tokens after it.
+int gated_anchors(const GatedProblem& p) { return (p.seg + kGateAnchor - 1) / kGateAnchor; }
 
 template <int NP>
 cudaError_t backward(const GatedProblem& p, const void* Q, const void* K, const void* V,
                      const float* G, const float* S_in, const void* dO, const float* dS_out,
                      void* dQ, void* dK, void* dV, float* dG, float* dS_in, float* ws,
                      cudaStream_t s) {
-  constexpr int kStages = NP == 1 ? 4 : 2;
+  constexpr int NB = kBlocks<NP>, kStages = 2;
   const long long BH = 1LL * p.B * p.H;
   Walk a = {};
-  a.anchor = p.seg < kGateAnchor ? p.seg : kGateAnchor;
-  a.nanchor = (p.N + a.anchor - 1) / a.anchor + 1;
+  a.anchor = kGateAnchor;
+  a.per_seg = gated_anchors(p);
   float* states = ws;
   float* grads = states + BH * p.nseg * 1024;
   a.anchors = grads + BH * p.nseg * 1024;
-  a.rows = a.anchors + BH * a.nanchor * 1024;
+  a.rows = a.anchors + BH * (1LL * p.nseg * a.per_seg + 1) * 1024;
   float* decays = a.rows + (BH * p.N + 3) / 4 * 4;
   cudaError_t e;
   if (p.nseg > 1) {
     auto seg = segment_kernel<NP, true, kStages>;
-    const int bytes = kWarps * Smem<NP, 4, kStages>::kWarp;
+    const int bytes = kWarps * Smem<NP, NB, 4, kStages>::kWarp;
     if ((e = allow_smem(seg, bytes)) != cudaSuccess) return e;
     seg<<<grid_of(BH * p.nseg), kWarps * 32, bytes, s>>>(p, Q, K, V, dO, G, states, grads, decays);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    combine_kernel<false><<<dim3(static_cast<unsigned>(BH), 2), 256, 0, s>>>(
-        static_cast<int>(BH), p.nseg, decays, states, S_in, grads, dS_out);
+    combine_kernel<false><<<dim3(static_cast<unsigned>(BH), 4, 2), 64, 0, s>>>(
+        p.nseg, decays, states, S_in, grads, dS_out);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   a.G = G;
@@ -667,8 +748,8 @@ cudaError_t backward(const GatedProblem& p, const void* Q, const void* K, const 
   a.o = dQ;
   a.init = S_in;
   a.prefix = states;
-  auto walk = walk_kernel<NP, true, NP == 1 ? 3 : 2>;
-  int bytes = kWarps * Smem<NP, 4, NP == 1 ? 3 : 2, 3>::kWarp;
+  auto walk = walk_kernel<NP, true, kStages>;
+  int bytes = kWarps * Smem<NP, NB, 4, kStages, 3>::kWarp;
   if ((e = allow_smem(walk, bytes)) != cudaSuccess) return e;
   walk<<<grid_of(BH * p.nseg), kWarps * 32, bytes, s>>>(a);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -683,7 +764,7 @@ cudaError_t backward(const GatedProblem& p, const void* Q, const void* K, const 
   a.prefix = grads;
   a.dG = dG;
   auto back = walk_back_kernel<NP, kStages>;
-  bytes = kWarps * Smem<NP, 4, kStages>::kWarp;
+  bytes = kWarps * Smem<NP, NB, 4, kStages>::kWarp;
   if ((e = allow_smem(back, bytes)) != cudaSuccess) return e;
   back<<<grid_of(BH * p.nseg), kWarps * 32, bytes, s>>>(a);
   return cudaGetLastError();
@@ -692,19 +773,15 @@ cudaError_t backward(const GatedProblem& p, const void* Q, const void* K, const 
 }  // namespace
 }  // namespace gated
 
-// Segments: as many as fill one wave of warps (16 on each of 148 SMs), none below 64
+// Segments: as many as fill one wave of warps (12 on each of 148 SMs), none below 64
 // tokens, where a warp's start and the extra states would cost more than they give.
-// The backward's segments are multiples of its anchors' distance.
-void gated_split(GatedProblem& p, bool backward) {
+void gated_split(GatedProblem& p) {
   const long long BH = 1LL * p.B * p.H;
-  const long long warps = 148LL * (backward ? 12 : 16);
-  long long n = BH > 0 ? warps / BH : 1;
+  long long n = BH > 0 ? 148LL * 12 / BH : 1;
   if (n < 1) n = 1;
   long long seg = (p.N + n - 1) / n;
   if (seg < 64) seg = 64;
-  long long unit = kGateBlock;
-  if (backward) unit = seg <= 64 ? 64 : seg <= 128 ? 128 : kGateAnchor;
-  seg = (seg + unit - 1) / unit * unit;
+  seg = (seg + 31) / 32 * 32;
   p.seg = static_cast<int>(seg);
   p.nseg = p.N > 0 ? static_cast<int>((p.N + seg - 1) / seg) : 1;
 }
@@ -713,9 +790,8 @@ size_t gated_workspace_floats(const GatedProblem& p, bool backward) {
   const size_t BH = static_cast<size_t>(p.B) * p.H;
   const size_t states = BH * p.nseg * 1024, decays = BH * p.nseg;
   if (!backward) return p.nseg > 1 ? states + decays : 0;
-  const int anchor = p.seg < kGateAnchor ? p.seg : kGateAnchor;
-  const size_t nanchor = static_cast<size_t>((p.N + anchor - 1) / anchor) + 1;
-  return 2 * states + BH * nanchor * 1024 + (BH * p.N + 3) / 4 * 4 + decays;
+  const size_t anchors = BH * (static_cast<size_t>(p.nseg) * gated::gated_anchors(p) + 1) * 1024;
+  return 2 * states + anchors + (BH * p.N + 3) / 4 * 4 + decays;
 }
 
 cudaError_t launch_gated(const GatedProblem& p, const void* Q, const void* K, const void* V,

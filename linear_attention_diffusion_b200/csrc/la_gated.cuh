@@ -78,13 +78,19 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
                                     uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-
+// c = a b: the first product of a sum, without zeroing registers for it.
+__device__ __forceinline__ void mma0(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                     uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
+}
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -110,6 +116,23 @@ __device__ __forceinline__ float hi_f(uint32_t x) { return __uint_as_float(x & 0
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Packed bf16 arithmetic, each result rounded once.
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t fma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t neg2(uint32_t a) {
+  uint32_t d;
+  asm("neg.bf16x2 %0, %1;" : "=r"(d) : "r"(a));
+  return d;
 }
 
 // Two float32 numbers as kParts pairs of bf16.
@@ -148,23 +171,24 @@ struct LaneOff {
 template <int NP>
 struct Frag {
   uint32_t r[NP][2][4];
-  __device__ __forceinline__ void rows(uint32_t tile, const LaneOff& o) {
+  // `plane`: bytes from one part of the tile to the next
+  __device__ __forceinline__ void rows(uint32_t tile, int plane, const LaneOff& o) {
 #pragma unroll
     for (int p = 0; p < NP; ++p)
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) ldsm4(r[p][ks], tile + p * kPlane + o.a[ks]);
+      for (int ks = 0; ks < 2; ++ks) ldsm4(r[p][ks], tile + p * plane + o.a[ks]);
   }
-  __device__ __forceinline__ void cols(uint32_t tile, const LaneOff& o) {
+  __device__ __forceinline__ void cols(uint32_t tile, int plane, const LaneOff& o) {
 #pragma unroll
     for (int p = 0; p < NP; ++p)
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) ldsm4(r[p][ks], tile + p * kPlane + o.b[ks]);
+      for (int ks = 0; ks < 2; ++ks) ldsm4(r[p][ks], tile + p * plane + o.b[ks]);
   }
-  __device__ __forceinline__ void deep(uint32_t tile, const LaneOff& o) {
+  __device__ __forceinline__ void deep(uint32_t tile, int plane, const LaneOff& o) {
 #pragma unroll
     for (int p = 0; p < NP; ++p)
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) ldsm4_t(r[p][ks], tile + p * kPlane + o.a[ks]);
+      for (int ks = 0; ks < 2; ++ks) ldsm4_t(r[p][ks], tile + p * plane + o.a[ks]);
   }
 };
 
@@ -174,29 +198,57 @@ constexpr __host__ __device__ bool pair_counts(int i, int j, int pa, int pb) {
   return i + j < (pa > pb ? pa : pb);
 }
 
+// Products of parts go into two sums, the leading one (part 0 x part 0) and the rest, which
+// are added at the end: the tensor cores cut a sum off after each step instead of rounding
+// it, and six more steps on the leading sum would cost it as many half steps.
+template <int kN>
+__device__ __forceinline__ void zero(float (&c)[kN][4]) {
+#pragma unroll
+  for (int i = 0; i < kN; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[i][j] = 0.0f;
+}
+template <int kN>
+__device__ __forceinline__ void add(float (&c)[kN][4], const float (&d)[kN][4]) {
+#pragma unroll
+  for (int i = 0; i < kN; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[i][j] += d[i][j];
+}
+
 // s[2] (16 tokens x 16 tokens) = A (tokens as rows) B (tokens as columns), over the dimensions.
 template <int NP>
 __device__ __forceinline__ void token_product(float (&s)[2][4], const Frag<NP>& A,
                                               const Frag<NP>& B) {
+  float rest[2][4];
 #pragma unroll
-  for (int nt = 0; nt < 2; ++nt)
+  for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[nt][i] = 0.0f;
+    for (int i = 0; i < NP; ++i)
 #pragma unroll
-  for (int i = 0; i < NP; ++i)
+      for (int j = 0; j < NP; ++j)
+        if (pair_counts(i, j, NP, NP)) {
 #pragma unroll
-    for (int j = 0; j < NP; ++j)
-      if (pair_counts(i, j, NP, NP)) {
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
-            mma(s[nt], A.r[i][ks], B.r[j][ks][2 * nt], B.r[j][ks][2 * nt + 1]);
-      }
+          for (int nt = 0; nt < 2; ++nt) {
+            const uint32_t b0 = B.r[j][ks][2 * nt], b1 = B.r[j][ks][2 * nt + 1];
+            if (i + j == 0) {
+              if (ks == 0)
+                mma0(s[nt], A.r[i][ks], b0, b1);
+              else
+                mma(s[nt], A.r[i][ks], b0, b1);
+            } else if (ks == 0 && i == 0 && j == 1) {
+              mma0(rest[nt], A.r[i][ks], b0, b1);
+            } else {
+              mma(rest[nt], A.r[i][ks], b0, b1);
+            }
+          }
+        }
+  if (NP > 1) add(s, rest);
 }
 
-// acc (16 tokens x 32) += W (16 x 16 weights, an accumulator) X (tokens as depth).
-template <int NP, int NC>
+// acc (16 tokens x 32) += W (16 x 16 weights, an accumulator) X (tokens as depth). kZero:
+// a quarter of W that is known to be 0 (2 nt + h), or -1.
+template <int NP, int NC, int kZero>
 __device__ __forceinline__ void weigh(float (&acc)[4][4], const float (&w)[2][4],
                                       const Frag<NP>& X) {
   uint32_t a[NC][4];
@@ -204,19 +256,28 @@ __device__ __forceinline__ void weigh(float (&acc)[4][4], const float (&w)[2][4]
   for (int i = 0; i < 4; ++i) {  // rows lo / hi of columns 0-7, then of columns 8-15
     uint32_t t[NC];
     const int nt = i >> 1, h = (i & 1) * 2;
-    split2<NC>(w[nt][h], w[nt][h + 1], t);
+    if (i != kZero) split2<NC>(w[nt][h], w[nt][h + 1], t);
 #pragma unroll
-    for (int p = 0; p < NC; ++p) a[p][i] = t[p];
+    for (int p = 0; p < NC; ++p) a[p][i] = i == kZero ? 0u : t[p];
   }
+  float rest[4][4];
 #pragma unroll
   for (int i = 0; i < NC; ++i)
 #pragma unroll
     for (int j = 0; j < NP; ++j)
       if (pair_counts(i, j, NC, NP)) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mma(acc[e], a[i], X.r[j][e >> 1][2 * (e & 1)], X.r[j][e >> 1][2 * (e & 1) + 1]);
+        for (int e = 0; e < 4; ++e) {  // four sums in turn: none waits for its own last step
+          const uint32_t b0 = X.r[j][e >> 1][2 * (e & 1)], b1 = X.r[j][e >> 1][2 * (e & 1) + 1];
+          if (NP == 1 || i + j == 0)
+            mma(acc[e], a[i], b0, b1);
+          else if (i == 0 && j == 1)
+            mma0(rest[e], a[i], b0, b1);
+          else
+            mma(rest[e], a[i], b0, b1);
+        }
       }
+  if (NP > 1) add(acc, rest);
 }
 
 // A 32 x 32 float32 state held as accumulators: st[mt][nt] covers rows 16 mt ..,
@@ -277,105 +338,161 @@ struct State {
         for (int i = 0; i < 4; ++i) p[outer<kTransposed>(mt, nt, i, lane)] = c[mt][nt][i];
   }
 
-  // state = decay * state + sum over tokens of w A^T B; A gives the rows, B the columns.
-  // w: the weights of tokens 2 (l % 4) + {0, 1, 8, 9}.
-  template <int NP, int NC>
-  __device__ __forceinline__ void update(float decay, const Frag<NP>& A, const Frag<NP>& B,
-                                         const float (&w)[4]) {
-    if (decay == 0.0f) {  // the same in all lanes: a stop drops the state whatever it holds
-      zero();
-    } else {
+  // state = decay * state + sum over the tokens of NB blocks of w A^T B; A gives the rows,
+  // B the columns, w[b] the weights of tokens 2 (l % 4) + {0, 1, 8, 9} of block b.
+  template <int NP, int NB>
+  __device__ __forceinline__ void update(float decay, const Frag<NP> (&A)[NB],
+                                         const Frag<NP> (&B)[NB], const float (&w)[NB][4]) {
+    constexpr int NC = NP == 1 ? 4 : 3;
+    if (decay == 0.0f) zero();  // the same in all lanes: a stop drops the state whatever it holds
+    uint32_t wp[NB][2][3];
+    if (NP == 1) {
 #pragma unroll
-      for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) c[mt][nt][i] *= decay;
+      for (int b = 0; b < NB; ++b) {
+        split2<3>(w[b][0], w[b][1], wp[b][0]);
+        split2<3>(w[b][2], w[b][3], wp[b][1]);
+      }
     }
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
-      uint32_t a[NC][4];
+      uint32_t a[NB][NC][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float x = 0.0f, y = 0.0f;
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int p = NP - 1; p >= 0; --p) {  // smallest part first: the sum is exact
-          x += lo_f(A.r[p][mt][i]);
-          y += hi_f(A.r[p][mt][i]);
+        for (int i = 0; i < 4; ++i) {
+          const int at = ((i & 1) << 1) | (i >> 1);  // registers 0, 2, 1, 3
+          if (NP == 1) {
+            // w = w0 + w1 + w2 in bf16 parts: v w0 is exactly its rounding and one more bf16;
+            // v w1 likewise, the latter with v w2 added. Packed arithmetic, five instructions
+            // for two numbers where a float32 product split three ways takes fifteen.
+            const uint32_t(&x)[3] = wp[b][i & 1];
+            const uint32_t v = A[b].r[0][mt][i];
+            const uint32_t p0 = mul2(v, x[0]), p2 = mul2(v, x[1]);
+            a[b][0][at] = p0;
+            a[b][1][at] = fma2(v, x[0], neg2(p0));
+            a[b][NC - 2][at] = p2;
+            a[b][NC - 1][at] = fma2(v, x[2], fma2(v, x[1], neg2(p2)));
+          } else {
+            float f = 0.0f, g = 0.0f;
+#pragma unroll
+            for (int p = NP - 1; p >= 0; --p) {  // smallest part first: the sum is exact
+              f += lo_f(A[b].r[p][mt][i]);
+              g += hi_f(A[b].r[p][mt][i]);
+            }
+            uint32_t t[NC];
+            split2<NC>(f * w[b][2 * (i & 1)], g * w[b][2 * (i & 1) + 1], t);
+#pragma unroll
+            for (int p = 0; p < NC; ++p) a[b][p][at] = t[p];
+          }
         }
-        uint32_t t[NC];
-        split2<NC>(x * w[2 * (i & 1)], y * w[2 * (i & 1) + 1], t);
-        const int at = ((i & 1) << 1) | (i >> 1);  // registers 0, 2, 1, 3
+      // the blocks' own sum by itself, so that the state is rounded once
+      float own[4][4], rest[4][4];
 #pragma unroll
-        for (int p = 0; p < NC; ++p) a[p][at] = t[p];
-      }
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int i = 0; i < NC; ++i)
 #pragma unroll
           for (int j = 0; j < NP; ++j)
-            if (pair_counts(i, j, NC, NP))
-              mma(c[mt][nt], a[i], B.r[j][nt >> 1][2 * (nt & 1)],
-                  B.r[j][nt >> 1][2 * (nt & 1) + 1]);
+            if (pair_counts(i, j, NC, NP)) {
+#pragma unroll
+              for (int nt = 0; nt < 4; ++nt) {
+                const uint32_t b0 = B[b].r[j][nt >> 1][2 * (nt & 1)],
+                               b1 = B[b].r[j][nt >> 1][2 * (nt & 1) + 1];
+                if (NP == 1 || i + j == 0) {
+                  if (b == 0 && i == 0)
+                    mma0(own[nt], a[b][i], b0, b1);
+                  else
+                    mma(own[nt], a[b][i], b0, b1);
+                } else if (b == 0 && i == 0 && j == 1) {
+                  mma0(rest[nt], a[b][i], b0, b1);
+                } else {
+                  mma(rest[nt], a[b][i], b0, b1);
+                }
+              }
+            }
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          c[mt][nt][i] = fmaf(c[mt][nt][i], decay, NP > 1 ? own[nt][i] + rest[nt][i] : own[nt][i]);
     }
   }
 
-  // acc (16 tokens x 32) += X (tokens as rows; depth = this state's columns) state^T.
-  template <int NP, int NC>
-  __device__ __forceinline__ void apply(float (&acc)[4][4], const Frag<NP>& X) const {
+  // acc[b] (16 tokens x 32) = X[b] (tokens as rows; depth = this state's columns) state^T,
+  // the state in NC parts.
+  template <int NP, int NC, int NB>
+  __device__ __forceinline__ void apply(float (&acc)[NB][4][4], const Frag<NP> (&X)[NB]) const {
+    float rest[NB][4][4];
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks)
+    for (int ks = 0; ks < 2; ++ks) {  // 16 columns of the state
+      uint32_t b0[4][NC], b1[4][NC];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        uint32_t b0[NC], b1[NC];
+      for (int e = 0; e < 4; ++e) {  // 8 rows of the state
         const int h = 2 * (e & 1);
-        split2<NC>(c[e >> 1][2 * ks][h], c[e >> 1][2 * ks][h + 1], b0);
-        split2<NC>(c[e >> 1][2 * ks + 1][h], c[e >> 1][2 * ks + 1][h + 1], b1);
-#pragma unroll
-        for (int i = 0; i < NP; ++i)
-#pragma unroll
-          for (int j = 0; j < NC; ++j)
-            if (pair_counts(i, j, NP, NC)) mma(acc[e], X.r[i][ks], b0[j], b1[j]);
+        split2<NC>(c[e >> 1][2 * ks][h], c[e >> 1][2 * ks][h + 1], b0[e]);
+        split2<NC>(c[e >> 1][2 * ks + 1][h], c[e >> 1][2 * ks + 1][h + 1], b1[e]);
       }
+      product<NP, NC, NB>(acc, rest, X, ks, b0, b1);
+    }
+    if (NP > 1) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) add(acc[b], rest[b]);
+    }
   }
-  // The same, and acc_t += Y (depth = this state's rows) state, from the same parts:
-  // an 8x8 tile turned over is the other product's operand.
-  template <int NP, int NC>
-  __device__ __forceinline__ void apply_both(float (&acc)[4][4], const Frag<NP>& X,
-                                             float (&acc_t)[4][4], const Frag<NP>& Y) const {
+  // acc[b] = Y[b] (tokens as rows; depth = this state's rows) state: an 8x8 tile of the
+  // state turned over is the operand.
+  template <int NP, int NC, int NB>
+  __device__ __forceinline__ void apply_turned(float (&acc)[NB][4][4],
+                                               const Frag<NP> (&Y)[NB]) const {
+    float rest[NB][4][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e)      // 8 rows of the state
+    for (int mt = 0; mt < 2; ++mt) {
+      uint32_t b0[4][NC], b1[4][NC];
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {  // 16 columns of the state
-        uint32_t b0[NC], b1[NC];
-        const int h = 2 * (e & 1);
-        split2<NC>(c[e >> 1][2 * ks][h], c[e >> 1][2 * ks][h + 1], b0);
-        split2<NC>(c[e >> 1][2 * ks + 1][h], c[e >> 1][2 * ks + 1][h + 1], b1);
-#pragma unroll
-        for (int i = 0; i < NP; ++i)
-#pragma unroll
-          for (int j = 0; j < NC; ++j)
-            if (pair_counts(i, j, NP, NC)) mma(acc[e], X.r[i][ks], b0[j], b1[j]);
-      }
-#pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {  // 16 rows (depth) x 8 columns
-        uint32_t b0[NC], b1[NC];
-        split2<NC>(c[mt][nt][0], c[mt][nt][1], b0);
-        split2<NC>(c[mt][nt][2], c[mt][nt][3], b1);
+      for (int nt = 0; nt < 4; ++nt) {
+        split2<NC>(c[mt][nt][0], c[mt][nt][1], b0[nt]);
+        split2<NC>(c[mt][nt][2], c[mt][nt][3], b1[nt]);
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
-          b0[j] = transpose8(b0[j]);
-          b1[j] = transpose8(b1[j]);
+          b0[nt][j] = transpose8(b0[nt][j]);
+          b1[nt][j] = transpose8(b1[nt][j]);
         }
-#pragma unroll
-        for (int i = 0; i < NP; ++i)
-#pragma unroll
-          for (int j = 0; j < NC; ++j)
-            if (pair_counts(i, j, NP, NC)) mma(acc_t[nt], Y.r[i][mt], b0[j], b1[j]);
       }
+      product<NP, NC, NB>(acc, rest, Y, mt, b0, b1);
+    }
+    if (NP > 1) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) add(acc[b], rest[b]);
+    }
+  }
+  // One step of depth 16 of the two above: 4 NB sums in turn.
+  template <int NP, int NC, int NB>
+  static __device__ __forceinline__ void product(float (&acc)[NB][4][4], float (&rest)[NB][4][4],
+                                                 const Frag<NP> (&X)[NB], int ks,
+                                                 const uint32_t (&b0)[4][NC],
+                                                 const uint32_t (&b1)[4][NC]) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i)
+#pragma unroll
+      for (int j = 0; j < NC; ++j)
+        if (pair_counts(i, j, NP, NC)) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const bool first = ks == 0 && i == 0;
+              if (NP == 1 || i + j == 0) {
+                if (first && j == 0)
+                  mma0(acc[b][e], X[b].r[i][ks], b0[e][j], b1[e][j]);
+                else
+                  mma(acc[b][e], X[b].r[i][ks], b0[e][j], b1[e][j]);
+              } else if (first && j == 1) {
+                mma0(rest[b][e], X[b].r[i][ks], b0[e][j], b1[e][j]);
+              } else {
+                mma(rest[b][e], X[b].r[i][ks], b0[e][j], b1[e][j]);
+              }
+            }
+        }
   }
   __device__ __forceinline__ float dot(const State& o) const {
     float s = 0.0f;
@@ -391,102 +508,165 @@ struct State {
   }
 };
 
-// Scale one row of an accumulator; a factor of zero drops it whatever it holds.
+// Scale one row of an accumulator; kHard: a factor of zero drops it whatever it holds.
+template <bool kHard>
 __device__ __forceinline__ void scale_row(float (&acc)[4][4], int h, float f) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    acc[e][2 * h] = f == 0.0f ? 0.0f : acc[e][2 * h] * f;
-    acc[e][2 * h + 1] = f == 0.0f ? 0.0f : acc[e][2 * h + 1] * f;
-  }
+  for (int e = 0; e < 4; ++e)
+#pragma unroll
+    for (int i = 2 * h; i < 2 * h + 2; ++i)
+      acc[e][i] = kHard && f == 0.0f ? 0.0f : acc[e][i] * f;
 }
 
-// The decays of a block of 16 tokens. Lane l stands for token i = l % 16; c is the sum of
-// log2 gates from the block's first token to token i (stops left out), kept as a float32
-// and what its rounding left: a decay is the difference of two sums, and gates of -100
-// would otherwise cost the small gates next to them 7 bits of their exponent.
+// The decays of NB blocks of 16 tokens. Lane l stands for token l % (16 NB); c is the sum of
+// log2 gates from its block's first token to it, stops left out.
+//
+// A decay is the difference of two such sums. Where a sum passes kEasy in size (and always for
+// float32 tensors) the sums carry what their rounding left in `low`, so that gates of -100 do
+// not cost the small gates next to them their low bits; below it the difference is good to
+// 2^-19. Stops are minded only where there are any (`hard`). Each is one branch for the warp.
+template <int NP, int NB>
 struct Decay {
-  float c, low;    // sum at token i: c + low
-  float last, last_low;  // the same at the block's last token
-  uint32_t stops;  // bit i: token i's gate lets nothing through
+  static constexpr float kEasy = NP == 1 ? -16.0f : 1.0f;
+  float c, low;          // sum at the lane's token: c + low
+  float last, last_low;  // the same at the last token of its block
+  uint32_t stops;        // bit i: token i's gate lets nothing through
+  bool wide, hard;
   __device__ __forceinline__ Decay(float g, int lane) {
     float x = g * kLog2e;
     const bool stop = x < kStop;
-    stops = __ballot_sync(0xffffffffu, stop) & 0xffffu;
+    stops = __ballot_sync(0xffffffffu, stop);
+    if (NB == 1) stops &= 0xffffu;
     if (stop) x = 0.0f;
-    low = 0.0f;
+    const float x0 = x;
+    low = last_low = 0.0f;
 #pragma unroll
     for (int d = 1; d < 16; d <<= 1) {
       const float y = __shfl_up_sync(0xffffffffu, x, d, 16);
-      const float yl = __shfl_up_sync(0xffffffffu, low, d, 16);
-      if ((lane & 15) >= d) {
-        const float s = __fadd_rn(x, y), t = __fsub_rn(s, x);  // s + what it rounds off
-        low += yl + (__fsub_rn(x, __fsub_rn(s, t)) + __fsub_rn(y, t));
-        x = s;
-      }
+      if ((lane & 15) >= d) x += y;
     }
     c = x;
-    last = __shfl_sync(0xffffffffu, c, 15);
-    last_low = __shfl_sync(0xffffffffu, low, 15);
+    hard = stops != 0;
+    wide = NP > 1 || __any_sync(0xffffffffu, !(c >= kEasy));
+    if (wide) {
+      x = x0;
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) {
+        const float y = __shfl_up_sync(0xffffffffu, x, d, 16);
+        const float yl = __shfl_up_sync(0xffffffffu, low, d, 16);
+        if ((lane & 15) >= d) {
+          const float s = __fadd_rn(x, y), t = __fsub_rn(s, x);  // s + what it rounds off
+          low += yl + (__fsub_rn(x, __fsub_rn(s, t)) + __fsub_rn(y, t));
+          x = s;
+        }
+      }
+      c = x;
+      last_low = __shfl_sync(0xffffffffu, low, 15, 16);
+    }
+    last = __shfl_sync(0xffffffffu, c, 15, 16);
   }
-  // from the state before the block to token i
+  // stops of the lane's own block
+  __device__ __forceinline__ uint32_t own_stops(int lane) const {
+    return NB == 1 ? stops : (stops >> (lane & 16)) & 0xffffu;
+  }
+  // from the state before the lane's block to its token
   __device__ __forceinline__ float head(int lane) const {
-    return (stops & ((2u << (lane & 15)) - 1u)) ? 0.0f : exp2_fast(c);
+    const float f = exp2_fast(c);
+    return hard && (own_stops(lane) & ((2u << (lane & 15)) - 1u)) ? 0.0f : f;
   }
-  // from token i to the block's end
+  // from the lane's token to its block's end
   __device__ __forceinline__ float tail(int lane) const {
-    return (stops >> ((lane & 15) + 1)) ? 0.0f : exp2_fast((last - c) + (last_low - low));
+    const float f = exp2_fast((last - c) + (last_low - low));
+    return hard && (own_stops(lane) >> ((lane & 15) + 1)) ? 0.0f : f;
   }
-  __device__ __forceinline__ float whole() const { return stops ? 0.0f : exp2_fast(last); }
-  // of `x`, one value per token: the values of tokens 2 (l % 4) + {0, 1, 8, 9}
-  static __device__ __forceinline__ void spread(float x, int lane, float (&out)[4]) {
-    const int j = 2 * (lane & 3);
+  // over the whole of the lane's block
+  __device__ __forceinline__ float whole(int lane) const {
+    return own_stops(lane) ? 0.0f : exp2_fast(last);
+  }
+  // of `x`, one value per token: the values of tokens 16 b + 2 (l % 4) + {0, 1, 8, 9}
+  static __device__ __forceinline__ void spread(float x, int b, int lane, float (&out)[4]) {
+    const int j = 16 * b + 2 * (lane & 3);
     out[0] = __shfl_sync(0xffffffffu, x, j);
     out[1] = __shfl_sync(0xffffffffu, x, j + 1);
     out[2] = __shfl_sync(0xffffffffu, x, j + 8);
     out[3] = __shfl_sync(0xffffffffu, x, j + 9);
   }
-  // Decays of an accumulator of 16 x 16 tokens: l[h][x] belongs to row token l / 4 + 8 h
-  // and column token 2 (l % 4) + {0, 1, 8, 9}; from the earlier to the later of the two,
-  // rows the later ones (kRowsLater) or the earlier ones. Pairs in the other order, or with
-  // a stop between them (the later token's own included), give 0.
-  template <bool kRowsLater>
-  __device__ __forceinline__ void between(int lane, float (&l)[2][4]) const {
-    float cc[4], cl[4];
-    spread(c, lane, cc);
-    spread(low, lane, cl);
+  // and of tokens 16 b + l / 4 + {0, 8}
+  static __device__ __forceinline__ void spread_rows(float x, int b, int lane, float (&out)[2]) {
+    out[0] = __shfl_sync(0xffffffffu, x, 16 * b + (lane >> 2));
+    out[1] = __shfl_sync(0xffffffffu, x, 16 * b + (lane >> 2) + 8);
+  }
+  // Decays of an accumulator of 16 x 16 tokens of block b: l[h][x] belongs to row token
+  // l / 4 + 8 h and column token 2 (l % 4) + {0, 1, 8, 9}; from the earlier to the later of
+  // the two, rows the later ones (kRowsLater) or the earlier ones. Pairs in the other order,
+  // or with a stop between them (the later token's own included), give 0. Of the four quarters
+  // one is all zeros: columns 8-15 of rows 0-7, or rows 8-15 of columns 0-7.
+  template <bool kRowsLater, bool kHard>
+  __device__ __forceinline__ void within(int b, int lane, float (&l)[2][4]) const {
+    float cc[4], cr[2], cl[4] = {0.0f, 0.0f, 0.0f, 0.0f}, lr[2] = {0.0f, 0.0f};
+    spread(c, b, lane, cc);
+    spread_rows(c, b, lane, cr);
+    if (wide) {
+      spread(low, b, lane, cl);
+      spread_rows(low, b, lane, lr);
+    }
+    const uint32_t st = (stops >> (16 * b)) & 0xffffu;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int row = (lane >> 2) + 8 * h;
-      const float cr = __shfl_sync(0xffffffffu, c, row);
-      const float lr = __shfl_sync(0xffffffffu, low, row);
-      int first, end;  // the column tokens that count
-      if (kRowsLater) {
-        const uint32_t before = stops & ((2u << row) - 1u);
-        first = before != 0 ? 31 - __clz(before) : 0;
-        end = row + 1;
-      } else {
-        const uint32_t after = stops & ~((2u << row) - 1u);
-        first = row;
-        end = after != 0 ? __ffs(after) - 1 : 16;
+      int first = 0, end = 0;  // the column tokens that count
+      if (kHard) {
+        if (kRowsLater) {
+          const uint32_t before = st & ((2u << row) - 1u);
+          first = before != 0 ? 31 - __clz(before) : 0;
+          end = row + 1;
+        } else {
+          const uint32_t after = st & ~((2u << row) - 1u);
+          first = row;
+          end = after != 0 ? __ffs(after) - 1 : 16;
+        }
       }
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
         const int col = 2 * (lane & 3) + (x & 1) + 8 * (x >> 1);
-        const float d = (cr - cc[x]) + (lr - cl[x]);
-        l[h][x] = (col >= first && col < end) ? exp2_fast(kRowsLater ? d : -d) : 0.0f;
+        const bool same = h == (x >> 1);  // a quarter on the diagonal
+        if (!same && (h == 1) != kRowsLater) {
+          l[h][x] = 0.0f;
+          continue;
+        }
+        float d = kRowsLater ? cr[h] - cc[x] : cc[x] - cr[h];
+        if (wide) d += kRowsLater ? lr[h] - cl[x] : cl[x] - lr[h];
+        if (kHard) {
+          l[h][x] = col >= first && col < end ? exp2_fast(d) : 0.0f;
+        } else {
+          const float f = exp2_fast(d);
+          l[h][x] = same && (kRowsLater ? col > row : col < row) ? 0.0f : f;
+        }
       }
     }
   }
 };
 
-// Shared memory of one warp: kStages stages of NT tiles and two lines of 16 floats
-// (the gates and one more value per token); float32 tiles arrive as they are and are
-// split into three bf16 planes before use (the first NS of them).
-template <int NP, int NT, int kStages, int NS = NT>
+// w *= l; kHard: a factor of zero drops the number whatever it is.
+template <bool kHard>
+__device__ __forceinline__ void decay_by(float (&w)[2][4], const float (&l)[2][4]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      float& e = w[x >> 1][2 * h + (x & 1)];
+      e = kHard && l[h][x] == 0.0f ? 0.0f : e * l[h][x];
+    }
+}
+
+// Shared memory of one warp: kStages stages of NT tiles of NB blocks; float32 tiles arrive as
+// they are and are split into three bf16 planes before use (the first NS of them).
+template <int NP, int NB, int NT, int kStages, int NS = NT>
 struct Smem {
-  static constexpr int kTile = NP == 1 ? kPlane : kGateBlock * 128;
-  static constexpr int kStage = NT * kTile + 128;
-  static constexpr int kPlanes = NP == 1 ? 0 : NS * 3 * kPlane;
+  static constexpr int kTile = NB * (NP == 1 ? kPlane : kGateBlock * 128);
+  static constexpr int kStage = NT * kTile + (NT == 4 ? 256 : 128);  // and a float or two per token
+  static constexpr int kPart = NB * kPlane;  // one plane of one tile
+  static constexpr int kPlanes = NP == 1 ? 0 : NS * 3 * kPart;
   static constexpr int kWarp = kStages * kStage + kPlanes;
 };
 
@@ -496,78 +676,198 @@ __device__ __forceinline__ uint32_t tile_off_f32(int row, int c16) {
   return static_cast<uint32_t>(row * 128 + ((c16 ^ (row & 1)) << 4));
 }
 
-// Start the copy of tokens [n0, n0 + 16) of one head; rows at or past `N` become zero.
-template <int NP>
-__device__ __forceinline__ void load_tile(uint32_t dst, const typename Io<NP>::T* base,
-                                          size_t stride, int n0, int N, int lane) {
-  constexpr int kRow = NP == 1 ? 4 : 8;  // 16-byte chunks of a row
-  constexpr int kElems = NP == 1 ? 8 : 4;
+// The ring of stages that a warp fills from global memory while it works: NT tiles of NB
+// blocks each, then the gates, then (NT = 4) one more float per token. A lane copies one
+// 16-byte chunk of every eighth (bf16) or fourth (float32) row and keeps its own pointers,
+// which move on by a step: computed afresh, the addresses took a third of all instructions.
+template <int NP, int NB, int NT, int kStages, int NS, bool kBackwards, bool kExtra>
+struct Ring {
+  using T = typename Io<NP>::T;
+  using M = Smem<NP, NB, NT, kStages, NS>;
+  static constexpr int kStep = NB * kGateBlock;
+  static constexpr int kChunks = NP == 1 ? 4 : 8;  // of a row
+  static constexpr int kRows = 32 / kChunks;       // rows of one copy of the warp
+  static constexpr int kCopies = kStep / kRows;
+  static constexpr int kPitch = kRows * (NP == 1 ? 64 : 128);
+  const char* src[NT];   // the lane's first chunk of the next step to copy
+  const float *gate, *extra;
+  int pitch, H;          // bytes of a token in the tensors; heads
+  int left;              // tokens from the next step on; backwards: of it (the first may be short)
+  int todo;              // steps still to copy
+  uint32_t end, dst, cur;  // shared memory: past the ring, the lane's place in the next stage, the
+                           // stage at hand
+
+  // `heads`: each tensor at token 0 of the head; first: the first step's first token;
+  // last: the segment's end.
+  __device__ __forceinline__ Ring(uint32_t smem, const T* const (&heads)[NT], const float* G,
+                                  int heads_per_token, const float* per_token, int first, int last,
+                                  int steps, int lane) {
+    H = heads_per_token;
+    pitch = H * 32 * static_cast<int>(sizeof(T));
+    const int row = lane / kChunks, c = lane % kChunks, i = lane & (kStep - 1);
 #pragma unroll
-  for (int i = 0; i < kRow / 2; ++i) {
-    const int idx = lane + 32 * i, row = idx / kRow, c = idx % kRow;
-    const bool in = n0 + row < N;
-    const typename Io<NP>::T* src = base + (in ? static_cast<size_t>(n0 + row) * stride : 0) +
-                                    c * kElems;
-    cp16(dst + (NP == 1 ? tile_off(row, c) : tile_off_f32(row, c)), src, in ? 16 : 0);
+    for (int t = 0; t < NT; ++t)
+      src[t] = reinterpret_cast<const char*>(heads[t]) + static_cast<size_t>(first + row) * pitch +
+               c * 16;
+    gate = G + static_cast<size_t>(first + i) * H;
+    extra = kExtra ? per_token + first + i : nullptr;
+    left = last - first;
+    todo = steps;
+    end = smem + kStages * M::kStage;
+    dst = smem + (NP == 1 ? tile_off(row, c) : tile_off_f32(row, c));
+    cur = smem - M::kStage;
   }
+  // Start the copies of the next step (an empty group when there is none).
+  __device__ __forceinline__ void issue(int lane) {
+    if (todo > 0) {
+      const int row = lane / kChunks, c = lane % kChunks, i = lane & (kStep - 1);
+      const uint32_t line =
+          dst + (NT * M::kTile + lane * 4 - (NP == 1 ? tile_off(row, c) : tile_off_f32(row, c)));
+      const int down = kRows * pitch;
+      if (left >= kStep) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const char* p = src[t];
+#pragma unroll
+          for (int k = 0; k < kCopies; ++k, p += down)
+            cp16(dst + t * M::kTile + k * kPitch, p, 16);
+        }
+        cp4(line, gate, 4);
+        if (kExtra) cp4(line + 128, extra, 4);
+      } else {  // rows past the end become zero, and so do their gates
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int k = 0; k < kCopies; ++k) {
+            const bool in = row + k * kRows < left;
+            cp16(dst + t * M::kTile + k * kPitch,
+                 src[t] + (in ? k * static_cast<ptrdiff_t>(down) : -row * static_cast<ptrdiff_t>(pitch)),
+                 in ? 16 : 0);
+          }
+        const bool in = i < left;
+        cp4(line, in ? gate : gate - static_cast<ptrdiff_t>(i) * H, in ? 4 : 0);
+        if (kExtra) cp4(line + 128, in ? extra : extra - i, in ? 4 : 0);
+      }
+      const ptrdiff_t move = static_cast<ptrdiff_t>(kBackwards ? -kStep : kStep) * pitch;
+#pragma unroll
+      for (int t = 0; t < NT; ++t) src[t] += move;
+      gate += static_cast<ptrdiff_t>(kBackwards ? -kStep : kStep) * H;
+      if (kExtra) extra += kBackwards ? -kStep : kStep;
+      left = kBackwards ? kStep : left - kStep;  // only the segment's last step can be short
+      --todo;
+      dst += M::kStage;
+      if (dst >= end) dst -= kStages * M::kStage;
+    }
+    cp_commit();
+  }
+  // The next stage, filled and seen by all lanes; the one before is free and filled anew.
+  __device__ __forceinline__ uint32_t next(int lane) {
+    cp_wait<kStages - 2>();
+    __syncwarp();
+    issue(lane);
+    cur += M::kStage;
+    if (cur == end) cur -= kStages * M::kStage;
+    return cur;
+  }
+};
+
+// Float `i` of shared memory at `addr`.
+__device__ __forceinline__ float lds(uint32_t addr) {
+  float x;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+  return x;
+}
+__device__ __forceinline__ uint2 lds2(uint32_t addr) {
+  uint2 x;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(addr) : "memory");
+  return x;
+}
+__device__ __forceinline__ uint4 lds4(uint32_t addr) {
+  uint4 x;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "r"(addr)
+               : "memory");
+  return x;
+}
+__device__ __forceinline__ void sts(uint32_t addr, uint32_t x) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
+__device__ __forceinline__ void sts2(uint32_t addr, float x, float y) {
+  asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
+}
+__device__ __forceinline__ void sts4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
 }
 
 // float32 tile -> three bf16 planes.
-__device__ __forceinline__ void split_tile(const uint8_t* src, uint8_t* planes, int lane) {
+template <int NB>
+__device__ __forceinline__ void split_tile(uint32_t src, uint32_t planes, int lane) {
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < 2 * NB; ++i) {
     const int idx = lane + 32 * i, row = idx >> 2, c = idx & 3;
-    const float4 a = *reinterpret_cast<const float4*>(src + tile_off_f32(row, 2 * c));
-    const float4 b = *reinterpret_cast<const float4*>(src + tile_off_f32(row, 2 * c + 1));
+    const uint4 a = lds4(src + tile_off_f32(row, 2 * c));
+    const uint4 b = lds4(src + tile_off_f32(row, 2 * c + 1));
     uint32_t w[4][3];
-    split2<3>(a.x, a.y, w[0]);
-    split2<3>(a.z, a.w, w[1]);
-    split2<3>(b.x, b.y, w[2]);
-    split2<3>(b.z, b.w, w[3]);
+    split2<3>(__uint_as_float(a.x), __uint_as_float(a.y), w[0]);
+    split2<3>(__uint_as_float(a.z), __uint_as_float(a.w), w[1]);
+    split2<3>(__uint_as_float(b.x), __uint_as_float(b.y), w[2]);
+    split2<3>(__uint_as_float(b.z), __uint_as_float(b.w), w[3]);
 #pragma unroll
     for (int p = 0; p < 3; ++p)
-      *reinterpret_cast<uint4*>(planes + p * kPlane + tile_off(row, c)) =
-          make_uint4(w[0][p], w[1][p], w[2][p], w[3][p]);
+      sts4(planes + p * NB * kPlane + tile_off(row, c), w[0][p], w[1][p], w[2][p], w[3][p]);
   }
 }
 
-// acc (16 tokens x 32, accumulators) through shared memory to rows of the tensor.
+// Where a lane's accumulator numbers (rows l / 4 and + 8, columns 8 e + 2 (l % 4) and + 1) and
+// its 16-byte pieces of whole rows lie in a block's tile.
 template <int NP>
-__device__ __forceinline__ void store_tile(const float (&acc)[4][4], uint8_t* tile,
-                                           typename Io<NP>::T* base, size_t stride, int n0, int N,
-                                           int lane) {
-  const int r = lane >> 2, q = lane & 3;
+struct TileLane {
+  uint32_t acc[NP == 1 ? 4 : 4];  // per e, row l / 4; 8 rows down: kDown
+  uint32_t piece;
+  static constexpr int kDown = NP == 1 ? 512 : 1024;
+  static constexpr int kPieces = NP == 1 ? 2 : 4;   // of a lane
+  static constexpr int kRows = 16 / kPieces;        // rows between them
+  __device__ __forceinline__ explicit TileLane(int lane) {
+    const int r = lane >> 2, q = lane & 3;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      acc[e] = NP == 1 ? tile_off(r, e) + q * 4
+                       : tile_off_f32(r, 2 * e + (q >> 1)) + (q & 1) * 8;
+    piece = NP == 1 ? tile_off(lane >> 2, lane & 3) : tile_off_f32(lane >> 3, lane & 7);
+  }
+};
+
+// acc (16 tokens x 32, accumulators) through shared memory to rows of the tensor; `dst` is the
+// lane's first piece, `down` the bytes to its next.
+template <int NP>
+__device__ __forceinline__ void store_tile(const float (&acc)[4][4], uint32_t tile,
+                                           const TileLane<NP>& tl, char* dst, ptrdiff_t down,
+                                           int rows, int lane) {
 #pragma unroll
   for (int e = 0; e < 4; ++e)
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int row = r + 8 * h;
       if (NP == 1)
-        *reinterpret_cast<uint32_t*>(tile + tile_off(row, e) + q * 4) =
-            pack2(acc[e][2 * h], acc[e][2 * h + 1]);
+        sts(tile + tl.acc[e] + h * TileLane<NP>::kDown, pack2(acc[e][2 * h], acc[e][2 * h + 1]));
       else
-        *reinterpret_cast<float2*>(tile + tile_off_f32(row, 2 * e + (q >> 1)) + (q & 1) * 8) =
-            make_float2(acc[e][2 * h], acc[e][2 * h + 1]);
+        sts2(tile + tl.acc[e] + h * TileLane<NP>::kDown, acc[e][2 * h], acc[e][2 * h + 1]);
     }
   __syncwarp();
-  constexpr int kRow = NP == 1 ? 4 : 8;
-  constexpr int kElems = NP == 1 ? 8 : 4;
+  const int row = lane / (NP == 1 ? 4 : 8);
 #pragma unroll
-  for (int i = 0; i < kRow / 2; ++i) {
-    const int idx = lane + 32 * i, row = idx / kRow, c = idx % kRow;
-    const uint4 v = *reinterpret_cast<const uint4*>(
-        tile + (NP == 1 ? tile_off(row, c) : tile_off_f32(row, c)));
-    if (n0 + row < N)
-      *reinterpret_cast<uint4*>(base + static_cast<size_t>(n0 + row) * stride + c * kElems) = v;
+  for (int i = 0; i < TileLane<NP>::kPieces; ++i, dst += down) {
+    const uint4 v = lds4(tile + tl.piece + i * TileLane<NP>::kRows * (NP == 1 ? 64 : 128));
+    if (rows >= 16 || row + i * TileLane<NP>::kRows < rows) *reinterpret_cast<uint4*>(dst) = v;
   }
 }
 
 // Sum over the 32 dimensions of acc * X, X the tile as it lies in shared memory
 // (bf16 or float32): the values of tokens l / 4 and l / 4 + 8, in every lane of the four.
 template <int NP>
-__device__ __forceinline__ void row_dots(const float (&acc)[4][4], const uint8_t* tile, int lane,
-                                         float (&out)[2]) {
-  const int r = lane >> 2, q = lane & 3;
+__device__ __forceinline__ void row_dots(const float (&acc)[4][4], uint32_t tile,
+                                         const TileLane<NP>& tl, float (&out)[2]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     float s = 0.0f;
@@ -575,15 +875,13 @@ __device__ __forceinline__ void row_dots(const float (&acc)[4][4], const uint8_t
     for (int e = 0; e < 4; ++e) {
       float x, y;
       if (NP == 1) {
-        const uint32_t v =
-            *reinterpret_cast<const uint32_t*>(tile + tile_off(r + 8 * h, e) + q * 4);
+        const uint32_t v = __float_as_uint(lds(tile + tl.acc[e] + h * TileLane<NP>::kDown));
         x = lo_f(v);
         y = hi_f(v);
       } else {
-        const float2 v = *reinterpret_cast<const float2*>(
-            tile + tile_off_f32(r + 8 * h, 2 * e + (q >> 1)) + (q & 1) * 8);
-        x = v.x;
-        y = v.y;
+        const uint2 v = lds2(tile + tl.acc[e] + h * TileLane<NP>::kDown);
+        x = __uint_as_float(v.x);
+        y = __uint_as_float(v.y);
       }
       s = fmaf(acc[e][2 * h], x, fmaf(acc[e][2 * h + 1], y, s));
     }
