@@ -324,6 +324,42 @@ la_status la_gated_attention_backward(const la_gated_shape* shape, const void* Q
                                       void* dV, float* dG, float* dS_in, void* ws,
                                       size_t ws_bytes, la_stream stream);
 
+/* Rotary positions of queries and keys. Q [B, N, H, D] and K [B, N, Hk, D],
+ * dense, io_dtype; the first `rot` dimensions of every head turn in pairs, the
+ * others pass through. Pair k (0 <= k < rot / 2) turns by position * rate_k,
+ *   f_k = base^(-2k / rot)
+ *   scaling 0: rate_k = f_k
+ *   scaling 1 (linear):  rate_k = f_k / factor
+ *   scaling 2 (base):    f_k with base * factor^(rot / (rot - 2)) in place of base
+ *                        (rot = 2: f_0 = 1 whatever the base)
+ *   scaling 3 (parts):   rate_k = f_k (w + (1 - w) / factor), w = clamp((t - slow) /
+ *                        (fast - slow), 0, 1), t = original_length f_k / 2 pi: the turns
+ *                        that the pair makes over the original length */
+typedef struct {
+  int B, N;
+  int H, Hk;    /* heads of Q and of K; Hk = 0: there is no K */
+  int D;        /* head width: a multiple of 8 in [8, 256] */
+  int rot;      /* even, 0 <= rot <= D */
+  int io_dtype; /* LA_IO_BF16 or LA_IO_F32 */
+  int half;     /* 0: pairs (2k, 2k+1); 1: pairs (k, k + rot/2) */
+  int scaling;  /* 0 .. 3, above */
+  int inverse;  /* 1: turn by the negative angle (the gradient of the call with 0) */
+  int pos_rows; /* positions are [B, N] (1) or [N], the same for the whole batch (0) */
+  int pos_offset;         /* without positions, token n stands at pos_offset + n; >= 0 */
+  double base;            /* > 1 */
+  double factor;          /* scaling 1 to 3: >= 1 */
+  double original_length; /* scaling 3: > 0 */
+  double slow, fast;      /* scaling 3: 0 <= slow < fast */
+  double mscale;          /* factor of the turned dimensions (1; finite) */
+} la_rotary_shape;
+
+/* Qo = rotated Q, Ko = rotated K (K and Ko NULL when Hk = 0). positions: int32 device
+ * array, any value, or NULL (above). Qo may be Q and Ko may be K (in place); no other
+ * overlap is allowed. Angles are formed and reduced in float64, the products are float32,
+ * bf16 results are rounded once; passed dimensions keep their bits. One launch. */
+la_status la_rotary(const la_rotary_shape* shape, const void* Q, const void* K,
+                    const int* positions, void* Qo, void* Ko, la_stream stream);
+
 /* Reset of the KV cache at the start of a video (SANA-Video section 4: the
  * cache starts empty): S[B,H,D,D] = 0, z[B,H,D] = 0 on `stream`. */
 la_status la_state_reset(float* S, float* z, int B, int H, int D,

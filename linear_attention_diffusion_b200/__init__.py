@@ -61,6 +61,15 @@ class LaGatedShape(ctypes.Structure):
     ]
 
 
+class LaRotaryShape(ctypes.Structure):
+    """Mirror of ``la_rotary_shape`` in include/la.h."""
+
+    _fields_ = [(n, ctypes.c_int) for n in (
+        "B", "N", "H", "Hk", "D", "rot", "io_dtype", "half", "scaling", "inverse", "pos_rows",
+        "pos_offset")] + [(n, ctypes.c_double) for n in (
+            "base", "factor", "original_length", "slow", "fast", "mscale")]
+
+
 class LaError(RuntimeError):
     def __init__(self, status: int, func: str):
         self.status = status
@@ -104,6 +113,8 @@ _lib.la_gated_attention.argtypes = [_gated_p] + [_vp] * 8 + [_sz, _vp]
 _lib.la_gated_attention.restype = _i
 _lib.la_gated_attention_backward.argtypes = [_gated_p] + [_vp] * 13 + [_sz, _vp]
 _lib.la_gated_attention_backward.restype = _i
+_lib.la_rotary.argtypes = [ctypes.POINTER(LaRotaryShape)] + [_vp] * 6
+_lib.la_rotary.restype = _i
 _lib.la_state_reset.argtypes = [_vp, _vp, _i, _i, _i, _vp]
 _lib.la_state_reset.restype = _i
 _lib.la_status_string.argtypes = [_i]
@@ -260,6 +271,12 @@ def la_gated_attention_backward(shape: LaGatedShape, Q, K, V, G, S_in, dO, dS_ou
                                             _ptr(dQ), _ptr(dK), _ptr(dV), _ptr(dG), _ptr(dS_in),
                                             _ptr(ws), _nbytes(ws), _stream(stream)),
            "la_gated_attention_backward")
+
+
+def la_rotary(shape: LaRotaryShape, Q, K, positions, Qo, Ko, stream=None) -> None:
+    """Rotary positions of Q and K; K, Ko and positions may be None (see include/la.h)."""
+    _check(_lib.la_rotary(ctypes.byref(shape), _ptr(Q), _ptr(K), _ptr(positions), _ptr(Qo), _ptr(Ko),
+                          _stream(stream)), "la_rotary")
 
 
 def la_state_reset(S, z, B: int, H: int, D: int = HEAD_DIM, stream=None) -> None:
@@ -489,3 +506,61 @@ def gated_attention_backward(Q, K, V, G, dO, S_in=None, dS_out=None, scale: floa
         ws = torch.empty(la_gated_workspace_bytes(shape, True), dtype=torch.uint8, device=Q.device)
         la_gated_attention_backward(shape, Q, K, V, G, S_in, dO, dS_out, dQ, dK, dV, dG, dS, ws, st)
     return dQ, dK, dV, dG, dS
+
+
+_ROTARY_LAYOUTS = {"interleaved": 0, "half": 1}
+_ROTARY_SCALINGS = {"linear": 1, "base": 2, "parts": 3}
+
+
+def make_rotary_shape(B: int, N: int, H: int, Hk: int, D: int, io_dtype: str = "bf16",
+                      rot: Optional[int] = None, layout: str = "half", base: float = 10000.0,
+                      scaling=None, mscale: float = 1.0, inverse: bool = False,
+                      pos_rows: bool = False, offset: int = 0) -> LaRotaryShape:
+    """``scaling``: None, ("linear", factor), ("base", factor) or ("parts", factor,
+    original_length, slow, fast)."""
+    io = {"bf16": LA_IO_BF16, "f32": LA_IO_F32, "float32": LA_IO_F32}[io_dtype]
+    kind, factor, length, slow, fast = 0, 1.0, 1.0, 0.0, 1.0
+    if scaling is not None:
+        kind, factor = _ROTARY_SCALINGS[scaling[0]], scaling[1]
+        if len(scaling) != (5 if kind == 3 else 2):
+            raise ValueError(f"scaling {scaling!r}: wrong number of values")
+        if kind == 3:
+            length, slow, fast = scaling[2:]
+    return LaRotaryShape(B, N, H, Hk, D, D if rot is None else rot, io, _ROTARY_LAYOUTS[layout], kind,
+                         int(inverse), int(pos_rows), offset, base, factor, length, slow, fast, mscale)
+
+
+def rotary(Q, K=None, positions=None, offset: int = 0, rot: Optional[int] = None,
+           layout: str = "half", base: float = 10000.0, scaling=None, mscale: float = 1.0,
+           inverse: bool = False, out=None, stream=None):
+    """Q [B, N, H, D] and K [B, N, Hk, D] (or None) with rotary positions: returns (Qo, Ko).
+
+    ``positions``: int32 [N] or [B, N], or None for offset + n. ``rot``: dimensions that turn
+    (default: all). ``inverse`` turns back, which is the gradient. ``out``: (Qo, Ko), which may be
+    (Q, K) to work in place. Frequencies and ``scaling``: see make_rotary_shape and include/la.h."""
+    import torch
+    if Q.dim() != 4:
+        raise ValueError(f"Q must be [B, N, H, D], got {tuple(Q.shape)}")
+    B, N, H, D = Q.shape
+    io = _io_of(Q, "Q")
+    _need("Q", Q, Q.shape, Q.dtype, Q.device)
+    Hk = 0
+    if K is not None:
+        if K.dim() != 4:
+            raise ValueError(f"K must be [B, N, Hk, D], got {tuple(K.shape)}")
+        Hk = K.shape[2]
+        _need("K", K, (B, N, Hk, D), Q.dtype, Q.device)
+    rows = positions is not None and positions.dim() == 2
+    _need("positions", positions, (B, N) if rows else (N,), torch.int32, Q.device)
+    Qo, Ko = (None, None) if out is None else out
+    _need("out[0]", Qo, Q.shape, Q.dtype, Q.device)
+    _need("out[1]", Ko, (B, N, Hk, D), Q.dtype, Q.device)
+    shape = make_rotary_shape(B, N, H, Hk, D, io, rot, layout, base, scaling, mscale, inverse, rows,
+                              offset)
+    with _On(Q.device, stream) as st:
+        if Qo is None:
+            Qo = torch.empty_like(Q)
+        if Ko is None and K is not None:
+            Ko = torch.empty_like(K)
+        la_rotary(shape, Q, K, positions, Qo, Ko if K is not None else None, st)
+    return Qo, (Ko if K is not None else None)

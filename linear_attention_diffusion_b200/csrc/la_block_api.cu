@@ -1,6 +1,7 @@
 // C-ABI layer of the block operators of include/la.h: gated linear attention,
 // rotary positions, the gated residual with its norms.
 #include <cmath>
+#include <cstdint>
 
 #include "la.h"
 #include "la_block_internal.h"
@@ -162,6 +163,84 @@ la_status la_gated_attention_backward(const la_gated_shape* shape, const void* Q
   const cudaError_t e = launch_gated_backward(p, Q, K, V, G, S_in, dO, dS_out, dQ, dK, dV, dG,
                                               dS_in, static_cast<float*>(ws), st);
   if (e != cudaSuccess) return cuda_fail(e, "gated attention backward");
+  return LA_OK;
+}
+
+la_status la_rotary(const la_rotary_shape* shape, const void* Q, const void* K,
+                    const int* positions, void* Qo, void* Ko, la_stream stream) {
+  if (shape == nullptr) return fail(LA_ERR_INVALID_ARG, "shape is NULL");
+  const la_rotary_shape& s = *shape;
+  if (s.B < 0 || s.N < 0 || s.H < 0 || s.Hk < 0)
+    return fail(LA_ERR_INVALID_ARG, "negative size B=%d N=%d H=%d Hk=%d", s.B, s.N, s.H, s.Hk);
+  if (s.D < 8 || s.D % 8 != 0 || s.D > kRotaryMaxD)
+    return fail(LA_ERR_UNSUPPORTED, "head width D=%d (a multiple of 8 in [8, %d])", s.D, kRotaryMaxD);
+  if (s.rot < 0 || s.rot > s.D || s.rot % 2 != 0)
+    return fail(LA_ERR_INVALID_ARG, "rot=%d (even, at most D=%d)", s.rot, s.D);
+  if (s.io_dtype != LA_IO_BF16 && s.io_dtype != LA_IO_F32)
+    return fail(LA_ERR_INVALID_ARG, "io_dtype=%d", s.io_dtype);
+  if ((s.half | s.inverse | s.pos_rows) & ~1)
+    return fail(LA_ERR_INVALID_ARG, "half=%d, inverse=%d, pos_rows=%d (0 or 1)", s.half, s.inverse,
+                s.pos_rows);
+  if (s.scaling < 0 || s.scaling > 3) return fail(LA_ERR_INVALID_ARG, "scaling=%d", s.scaling);
+  if (s.pos_offset < 0 || 1LL * s.pos_offset + s.N > 0x7fffffffLL)
+    return fail(LA_ERR_INVALID_ARG, "pos_offset=%d", s.pos_offset);
+  if (!(std::isfinite(s.base) && s.base > 1.0))
+    return fail(LA_ERR_INVALID_ARG, "base must be finite and > 1");
+  if (!std::isfinite(s.mscale)) return fail(LA_ERR_INVALID_ARG, "mscale must be finite");
+  if (s.scaling != 0 && !(std::isfinite(s.factor) && s.factor >= 1.0))
+    return fail(LA_ERR_INVALID_ARG, "factor must be finite and >= 1");
+  if (s.scaling == 3 && !(std::isfinite(s.original_length) && s.original_length > 0.0 &&
+                          std::isfinite(s.slow) && std::isfinite(s.fast) && s.slow >= 0.0 &&
+                          s.slow < s.fast))
+    return fail(LA_ERR_INVALID_ARG, "original_length > 0 and 0 <= slow < fast are needed");
+  const double rows = 1.0 * s.B * s.N;
+  if (rows * s.D * (1.0 * s.H + s.Hk) >= 1.0 * (1LL << 40) || rows >= 1.0 * (1LL << 31) ||
+      (1LL * s.H + s.Hk) * s.D >= (1LL << 24))
+    return fail(LA_ERR_UNSUPPORTED, "tensor too large");
+  const bool any_q = rows > 0 && s.H > 0, any_k = rows > 0 && s.Hk > 0;
+  const size_t e = s.io_dtype == LA_IO_BF16 ? 2 : 4;
+  const size_t nr = static_cast<size_t>(s.B) * s.N;
+  const size_t nq = nr * s.H * s.D * e, nk = nr * s.Hk * s.D * e;
+  const size_t np = (s.pos_rows ? nr : static_cast<size_t>(s.N)) * 4;
+  LA_TRY(check_ptr(Q, "Q", any_q));
+  LA_TRY(check_ptr(Qo, "Qo", any_q));
+  LA_TRY(check_ptr(K, "K", any_k));
+  LA_TRY(check_ptr(Ko, "Ko", any_k));
+  if ((any_q || any_k) && (reinterpret_cast<uintptr_t>(positions) & 3u) != 0)
+    return fail(LA_ERR_INVALID_ARG, "positions are not 4-byte aligned");
+  const Buffer ins[] = {{Q == Qo ? nullptr : Q, nq, "Q"}, {K == Ko ? nullptr : K, nk, "K"},
+                        {positions, np, "positions"}};
+  const Buffer outs[] = {{Qo, nq, "Qo"}, {Ko, nk, "Ko"}};
+  if (any_q || any_k) LA_TRY(check_apart(outs, ins));
+  if (!any_q && !any_k) return LA_OK;
+  RotaryProblem p = {};
+  p.rows = static_cast<long long>(nr);
+  p.N = s.N;
+  p.H = s.H;
+  p.Hk = s.Hk;
+  p.D = s.D;
+  p.rot = s.rot;
+  p.io = s.io_dtype;
+  p.half = s.half;
+  p.inverse = s.inverse;
+  p.pos_rows = s.pos_rows;
+  p.pos_offset = s.pos_offset;
+  p.mscale = s.mscale;
+  double base = s.base;
+  if (s.scaling == 2 && s.rot > 2) base *= std::pow(s.factor, 1.0 * s.rot / (s.rot - 2));
+  for (int k = 0; k < s.rot / 2; ++k) {
+    double f = std::pow(base, -2.0 * k / s.rot);
+    if (s.scaling == 1) f /= s.factor;
+    if (s.scaling == 3) {
+      const double turns = s.original_length * f / 6.283185307179586476925286766559;
+      const double w = std::fmin(1.0, std::fmax(0.0, (turns - s.slow) / (s.fast - s.slow)));
+      f *= w + (1.0 - w) / s.factor;
+    }
+    p.rate[k] = f;
+  }
+  const cudaError_t err =
+      launch_rotary(p, Q, K, positions, Qo, Ko, reinterpret_cast<cudaStream_t>(stream));
+  if (err != cudaSuccess) return cuda_fail(err, "rotary");
   return LA_OK;
 }
 

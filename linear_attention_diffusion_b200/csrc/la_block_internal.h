@@ -32,4 +32,18 @@ cudaError_t launch_gated_backward(const GatedProblem& p, const void* Q, const vo
                                   const void* dO, const float* dS_out, void* dQ, void* dK,
                                   void* dV, float* dG, float* dS_in, float* ws, cudaStream_t s);
 
+// Rotary positions (la_rotary.cu).
+constexpr int kRotaryMaxD = 256;
+struct RotaryProblem {
+  long long rows;    // tokens over the whole batch
+  int N, H, Hk, D, rot;
+  int io, half, inverse;
+  int pos_rows;      // positions are [B, N] (1) or [N] (0)
+  int pos_offset;    // position of token 0 when there are no positions
+  double mscale;
+  double rate[kRotaryMaxD / 2];  // radians per position of each pair
+};
+cudaError_t launch_rotary(const RotaryProblem& p, const void* Q, const void* K, const int* pos,
+                          void* Qo, void* Ko, cudaStream_t s);
+
 }  // namespace la

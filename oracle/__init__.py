@@ -37,3 +37,4 @@ from .gated import (  # noqa: F401,E402
     gated_bruteforce,
     gated_magnitudes,
 )
+from .rotary import rotary, rotary_rates  # noqa: F401,E402
