@@ -360,6 +360,48 @@ typedef struct {
 la_status la_rotary(const la_rotary_shape* shape, const void* Q, const void* K,
                     const int* positions, void* Qo, void* Ko, la_stream stream);
 
+/* The end of one block and the start of the next: the gated residual with a norm after
+ * the block and a norm before the next one. x, f, h, y and their gradients are dense
+ * [B, N, C] tensors of io_dtype; parameters are float32, dense. */
+typedef struct {
+  int B, N;
+  int C;        /* a multiple of 8 in [8, 8192] */
+  int io_dtype; /* LA_IO_BF16 or LA_IO_F32 */
+  int norm;     /* of y: 0 RMS, 1 layer (the mean is subtracted) */
+  float eps;    /* added to the mean square, >= 0 and finite */
+  float alpha;  /* factor of the residual branch, finite */
+} la_norm_shape;
+
+/* u = f                                       (w_post NULL), or
+ * u = f / sqrt(mean(f^2) + eps) * w_post      (w_post [C])
+ * h = x + alpha gate_b u                      (gate [B, C]; NULL: 1)
+ * y = n w_pre (1 + mod_scale_b) + mod_shift_b, n = the RMS or layer norm of h over C
+ *                                             (w_pre [C], mod_* [B, C]; NULL: 1, 0, 0)
+ * f may be NULL (then gate, w_post and h must be): a plain norm with modulation. y or h
+ * may be NULL where it is not wanted, not both. h may be x or f, and y may be x or f,
+ * exactly; no other overlap is allowed, and h is not y. The norm of y is taken of h
+ * before its rounding. float32 arithmetic, each output rounded once. One launch. */
+la_status la_gate_residual_norm(const la_norm_shape* shape, const void* x, const void* f,
+                                const float* gate, const float* w_post, const float* w_pre,
+                                const float* mod_scale, const float* mod_shift, void* h, void* y,
+                                la_stream stream);
+
+/* Bytes of workspace la_gate_residual_norm_backward needs. 0 iff the shape is invalid. */
+size_t la_norm_workspace_bytes(const la_norm_shape* shape);
+
+/* Gradients of la_gate_residual_norm from dh and dy (one of the two may be NULL: zero):
+ * dx, df [B, N, C] io_dtype (df NULL iff f is); dgate, dmod_scale, dmod_shift [B, C] and
+ * dw_post, dw_pre [C] float32, each NULL where not wanted. dx may be dh or dy, and df may be
+ * dy or dh, exactly; no other overlap is allowed. Two launches (one without parameters'
+ * gradients). Deterministic. */
+la_status la_gate_residual_norm_backward(const la_norm_shape* shape, const void* x, const void* f,
+                                         const float* gate, const float* w_post,
+                                         const float* w_pre, const float* mod_scale,
+                                         const void* dh, const void* dy, void* dx, void* df,
+                                         float* dgate, float* dw_post, float* dw_pre,
+                                         float* dmod_scale, float* dmod_shift, void* ws,
+                                         size_t ws_bytes, la_stream stream);
+
 /* Reset of the KV cache at the start of a video (SANA-Video section 4: the
  * cache starts empty): S[B,H,D,D] = 0, z[B,H,D] = 0 on `stream`. */
 la_status la_state_reset(float* S, float* z, int B, int H, int D,

@@ -70,6 +70,15 @@ class LaRotaryShape(ctypes.Structure):
             "base", "factor", "original_length", "slow", "fast", "mscale")]
 
 
+class LaNormShape(ctypes.Structure):
+    """Mirror of ``la_norm_shape`` in include/la.h."""
+
+    _fields_ = [
+        ("B", ctypes.c_int), ("N", ctypes.c_int), ("C", ctypes.c_int), ("io_dtype", ctypes.c_int),
+        ("norm", ctypes.c_int), ("eps", ctypes.c_float), ("alpha", ctypes.c_float),
+    ]
+
+
 class LaError(RuntimeError):
     def __init__(self, status: int, func: str):
         self.status = status
@@ -115,6 +124,13 @@ _lib.la_gated_attention_backward.argtypes = [_gated_p] + [_vp] * 13 + [_sz, _vp]
 _lib.la_gated_attention_backward.restype = _i
 _lib.la_rotary.argtypes = [ctypes.POINTER(LaRotaryShape)] + [_vp] * 6
 _lib.la_rotary.restype = _i
+_norm_p = ctypes.POINTER(LaNormShape)
+_lib.la_gate_residual_norm.argtypes = [_norm_p] + [_vp] * 10
+_lib.la_gate_residual_norm.restype = _i
+_lib.la_norm_workspace_bytes.argtypes = [_norm_p]
+_lib.la_norm_workspace_bytes.restype = _sz
+_lib.la_gate_residual_norm_backward.argtypes = [_norm_p] + [_vp] * 16 + [_sz, _vp]
+_lib.la_gate_residual_norm_backward.restype = _i
 _lib.la_state_reset.argtypes = [_vp, _vp, _i, _i, _i, _vp]
 _lib.la_state_reset.restype = _i
 _lib.la_status_string.argtypes = [_i]
@@ -277,6 +293,36 @@ def la_rotary(shape: LaRotaryShape, Q, K, positions, Qo, Ko, stream=None) -> Non
     """Rotary positions of Q and K; K, Ko and positions may be None (see include/la.h)."""
     _check(_lib.la_rotary(ctypes.byref(shape), _ptr(Q), _ptr(K), _ptr(positions), _ptr(Qo), _ptr(Ko),
                           _stream(stream)), "la_rotary")
+
+
+def make_norm_shape(B: int, N: int, C: int, io_dtype: str = "bf16", norm: str = "layer",
+                    eps: float = 1e-6, alpha: float = 1.0) -> LaNormShape:
+    io = {"bf16": LA_IO_BF16, "f32": LA_IO_F32, "float32": LA_IO_F32}[io_dtype]
+    return LaNormShape(int(B), int(N), int(C), io, {"rms": 0, "layer": 1}[norm], float(eps),
+                       float(alpha))
+
+
+def la_gate_residual_norm(shape: LaNormShape, x, f, gate, w_post, w_pre, mod_scale, mod_shift, h, y,
+                          stream=None) -> None:
+    """Gated residual and norm; all but x may be None (see include/la.h)."""
+    _check(_lib.la_gate_residual_norm(ctypes.byref(shape), _ptr(x), _ptr(f), _ptr(gate), _ptr(w_post),
+                                      _ptr(w_pre), _ptr(mod_scale), _ptr(mod_shift), _ptr(h), _ptr(y),
+                                      _stream(stream)), "la_gate_residual_norm")
+
+
+def la_norm_workspace_bytes(shape: LaNormShape) -> int:
+    return int(_lib.la_norm_workspace_bytes(ctypes.byref(shape)))
+
+
+def la_gate_residual_norm_backward(shape: LaNormShape, x, f, gate, w_post, w_pre, mod_scale, dh, dy,
+                                   dx, df, dgate, dw_post, dw_pre, dmod_scale, dmod_shift, ws,
+                                   stream=None) -> None:
+    """Gradients of la_gate_residual_norm (see include/la.h for what may be None)."""
+    _check(_lib.la_gate_residual_norm_backward(
+        ctypes.byref(shape), _ptr(x), _ptr(f), _ptr(gate), _ptr(w_post), _ptr(w_pre),
+        _ptr(mod_scale), _ptr(dh), _ptr(dy), _ptr(dx), _ptr(df), _ptr(dgate), _ptr(dw_post),
+        _ptr(dw_pre), _ptr(dmod_scale), _ptr(dmod_shift), _ptr(ws), _nbytes(ws), _stream(stream)),
+        "la_gate_residual_norm_backward")
 
 
 def la_state_reset(S, z, B: int, H: int, D: int = HEAD_DIM, stream=None) -> None:
@@ -564,3 +610,59 @@ def rotary(Q, K=None, positions=None, offset: int = 0, rot: Optional[int] = None
             Ko = torch.empty_like(K)
         la_rotary(shape, Q, K, positions, Qo, Ko if K is not None else None, st)
     return Qo, (Ko if K is not None else None)
+
+
+def _norm_checks(x, f, gate, w_post, w_pre, mod_scale, mod_shift, **like_x):
+    import torch
+    if x.dim() != 3:
+        raise ValueError(f"x must be [B, N, C], got {tuple(x.shape)}")
+    io = _io_of(x, "x")
+    B, _, C = x.shape
+    for name, t in (("x", x), ("f", f), *like_x.items()):
+        _need(name, t, x.shape, x.dtype, x.device)
+    for name, t in (("gate", gate), ("mod_scale", mod_scale), ("mod_shift", mod_shift)):
+        _need(name, t, (B, C), torch.float32, x.device)
+    for name, t in (("w_post", w_post), ("w_pre", w_pre)):
+        _need(name, t, (C,), torch.float32, x.device)
+    return io
+
+
+def gate_residual_norm(x, f=None, gate=None, w_post=None, w_pre=None, mod_scale=None, mod_shift=None,
+                       norm: str = "layer", eps: float = 1e-6, alpha: float = 1.0, out=None,
+                       want_h: bool = True, want_y: bool = True, stream=None):
+    """h, y of the gated residual and the norms around it, for [B, N, C] CUDA tensors:
+
+    u = f, or RMSNorm(f) w_post;  h = x + alpha gate u;  y = norm(h) w_pre (1 + mod_scale) + mod_shift
+
+    with float32 parameters gate, mod_scale, mod_shift [B, C] and w_post, w_pre [C]. h is None
+    without f or with ``want_h=False``, y with ``want_y=False``. ``out``: (h, y), each of which
+    may be x or f."""
+    import torch
+    h, y = (None, None) if out is None else out
+    io = _norm_checks(x, f, gate, w_post, w_pre, mod_scale, mod_shift, h=h, y=y)
+    shape = make_norm_shape(*x.shape, io, norm, eps, alpha)
+    with _On(x.device, stream) as st:
+        if h is None and f is not None and want_h:
+            h = torch.empty_like(x)
+        if y is None and want_y:
+            y = torch.empty_like(x)
+        la_gate_residual_norm(shape, x, f, gate, w_post, w_pre, mod_scale, mod_shift, h, y, st)
+    return h, y
+
+
+def gate_residual_norm_backward(x, f, dy, dh, gate=None, w_post=None, w_pre=None, mod_scale=None,
+                                mod_shift=None, norm: str = "layer", eps: float = 1e-6,
+                                alpha: float = 1.0, stream=None):
+    """dx, df, dgate, dw_post, dw_pre, dmod_scale, dmod_shift of gate_residual_norm: None for what
+    was not given (dmod_shift with mod_shift). f, and one of dy and dh, may be None."""
+    import torch
+    io = _norm_checks(x, f, gate, w_post, w_pre, mod_scale, mod_shift, dy=dy, dh=dh)
+    shape = make_norm_shape(*x.shape, io, norm, eps, alpha)
+    with _On(x.device, stream) as st:
+        like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
+        dx, df, dgate, dwo, dwi, dsc, dsh = (like(t) for t in (x, f, gate, w_post, w_pre, mod_scale,
+                                                               mod_shift))
+        ws = torch.empty(la_norm_workspace_bytes(shape), dtype=torch.uint8, device=x.device)
+        la_gate_residual_norm_backward(shape, x, f, gate, w_post, w_pre, mod_scale, dh, dy, dx, df,
+                                       dgate, dwo, dwi, dsc, dsh, ws, st)
+    return dx, df, dgate, dwo, dwi, dsc, dsh

@@ -83,6 +83,26 @@ la_status pass_on(float* dst, const float* src, size_t bytes, cudaStream_t st) {
   return e == cudaSuccess ? LA_OK : cuda_fail(e, "state of an empty sequence");
 }
 
+la_status make_norm(const la_norm_shape* s, NormProblem& p) {
+  if (s == nullptr) return fail(LA_ERR_INVALID_ARG, "shape is NULL");
+  if (s->B < 0 || s->N < 0) return fail(LA_ERR_INVALID_ARG, "negative size B=%d N=%d", s->B, s->N);
+  if (s->C < 8 || s->C % 8 != 0 || s->C > kNormMaxC)
+    return fail(LA_ERR_UNSUPPORTED, "width C=%d (a multiple of 8 in [8, %d])", s->C, kNormMaxC);
+  if (s->io_dtype != LA_IO_BF16 && s->io_dtype != LA_IO_F32)
+    return fail(LA_ERR_INVALID_ARG, "io_dtype=%d", s->io_dtype);
+  if (s->norm != 0 && s->norm != 1) return fail(LA_ERR_INVALID_ARG, "norm=%d", s->norm);
+  if (!(std::isfinite(s->eps) && s->eps >= 0.0f))
+    return fail(LA_ERR_INVALID_ARG, "eps must be finite and >= 0");
+  if (!std::isfinite(s->alpha)) return fail(LA_ERR_INVALID_ARG, "alpha must be finite");
+  if (s->B > 65535 || s->N > (1 << 30) || 1.0 * s->B * s->N * s->C >= 1.0 * (1LL << 40))
+    return fail(LA_ERR_UNSUPPORTED, "tensor too large");
+  p = NormProblem{s->B, s->N, s->C, s->io_dtype, s->norm, s->eps, s->alpha, 1};
+  norm_split(p);
+  return LA_OK;
+}
+
+la_status check_param(const float* w, const char* name) { return check_ptr(w, name, w != nullptr); }
+
 }  // namespace
 
 extern "C" {
@@ -241,6 +261,115 @@ la_status la_rotary(const la_rotary_shape* shape, const void* Q, const void* K,
   const cudaError_t err =
       launch_rotary(p, Q, K, positions, Qo, Ko, reinterpret_cast<cudaStream_t>(stream));
   if (err != cudaSuccess) return cuda_fail(err, "rotary");
+  return LA_OK;
+}
+
+la_status la_gate_residual_norm(const la_norm_shape* shape, const void* x, const void* f,
+                                const float* gate, const float* w_post, const float* w_pre,
+                                const float* mod_scale, const float* mod_shift, void* h, void* y,
+                                la_stream stream) {
+  NormProblem p;
+  LA_TRY(make_norm(shape, p));
+  const bool any = p.B > 0 && p.N > 0;
+  if (f == nullptr && any && (gate != nullptr || w_post != nullptr || h != nullptr))
+    return fail(LA_ERR_INVALID_ARG, "without f there is no gate, w_post or h");
+  if (any && h == nullptr && y == nullptr) return fail(LA_ERR_INVALID_ARG, "h and y are both NULL");
+  LA_TRY(check_ptr(x, "x", any));
+  LA_TRY(check_ptr(f, "f", any && f != nullptr));
+  LA_TRY(check_ptr(h, "h", any && h != nullptr));
+  LA_TRY(check_ptr(y, "y", any && y != nullptr));
+  LA_TRY(check_param(gate, "gate"));
+  LA_TRY(check_param(w_post, "w_post"));
+  LA_TRY(check_param(w_pre, "w_pre"));
+  LA_TRY(check_param(mod_scale, "mod_scale"));
+  LA_TRY(check_param(mod_shift, "mod_shift"));
+  if (!any) return LA_OK;
+  const size_t n = static_cast<size_t>(p.B) * p.N * p.C * (p.io == LA_IO_BF16 ? 2 : 4);
+  const size_t nc = static_cast<size_t>(p.C) * 4, nb = nc * p.B;
+  const Buffer params[] = {{gate, nb, "gate"}, {w_post, nc, "w_post"}, {w_pre, nc, "w_pre"},
+                           {mod_scale, nb, "mod_scale"}, {mod_shift, nb, "mod_shift"}};
+  const Buffer outs[] = {{h, n, "h"}, {y, n, "y"}};
+  LA_TRY(check_apart(outs, params));
+  for (const Buffer& o : outs)  // x or f itself, but no part of it
+    for (const void* in : {x, f})
+      if (o.p != in && overlap(o.p, n, in, n))
+        return fail(LA_ERR_INVALID_ARG, "%s overlaps x or f without being it", o.name);
+  const cudaError_t e = launch_norm(p, x, f, NormParams{gate, w_post, w_pre, mod_scale, mod_shift},
+                                    h, y, reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "gated residual norm");
+  return LA_OK;
+}
+
+size_t la_norm_workspace_bytes(const la_norm_shape* shape) {
+  NormProblem p;
+  if (make_norm(shape, p) != LA_OK) return 0;
+  const size_t n = align256(norm_workspace_floats(p) * sizeof(float));
+  return n == 0 ? 256 : n;
+}
+
+la_status la_gate_residual_norm_backward(const la_norm_shape* shape, const void* x, const void* f,
+                                         const float* gate, const float* w_post,
+                                         const float* w_pre, const float* mod_scale,
+                                         const void* dh, const void* dy, void* dx, void* df,
+                                         float* dgate, float* dw_post, float* dw_pre,
+                                         float* dmod_scale, float* dmod_shift, void* ws,
+                                         size_t ws_bytes, la_stream stream) {
+  NormProblem p;
+  LA_TRY(make_norm(shape, p));
+  const bool any = p.B > 0 && p.N > 0;
+  if (any) {
+    if (f == nullptr && (gate != nullptr || w_post != nullptr || df != nullptr ||
+                         dgate != nullptr || dw_post != nullptr))
+      return fail(LA_ERR_INVALID_ARG, "without f there is no gate, w_post or gradient of them");
+    if (f != nullptr && df == nullptr) return fail(LA_ERR_INVALID_ARG, "df is NULL");
+    if (dh == nullptr && dy == nullptr)
+      return fail(LA_ERR_INVALID_ARG, "dh and dy are both NULL");
+  }
+  LA_TRY(check_ptr(x, "x", any));
+  LA_TRY(check_ptr(f, "f", any && f != nullptr));
+  LA_TRY(check_ptr(dh, "dh", any && dh != nullptr));
+  LA_TRY(check_ptr(dy, "dy", any && dy != nullptr));
+  LA_TRY(check_ptr(dx, "dx", any));
+  LA_TRY(check_ptr(df, "df", any && df != nullptr));
+  LA_TRY(check_param(gate, "gate"));
+  LA_TRY(check_param(w_post, "w_post"));
+  LA_TRY(check_param(w_pre, "w_pre"));
+  LA_TRY(check_param(mod_scale, "mod_scale"));
+  LA_TRY(check_param(dgate, "dgate"));
+  LA_TRY(check_param(dw_post, "dw_post"));
+  LA_TRY(check_param(dw_pre, "dw_pre"));
+  LA_TRY(check_param(dmod_scale, "dmod_scale"));
+  LA_TRY(check_param(dmod_shift, "dmod_shift"));
+  const size_t need = any ? align256(norm_workspace_floats(p) * sizeof(float)) : 0;
+  LA_TRY(check_workspace(ws, ws_bytes, need));
+  const size_t n = static_cast<size_t>(p.B) * p.N * p.C * (p.io == LA_IO_BF16 ? 2 : 4);
+  const size_t nc = static_cast<size_t>(p.C) * 4, nb = nc * p.B;
+  const Buffer ins[] = {{x, n, "x"}, {f, n, "f"}, {gate, nb, "gate"}, {w_post, nc, "w_post"},
+                        {w_pre, nc, "w_pre"}, {mod_scale, nb, "mod_scale"}};
+  const Buffer outs[] = {{dx, n, "dx"}, {df, n, "df"}, {dgate, nb, "dgate"},
+                         {dw_post, nc, "dw_post"}, {dw_pre, nc, "dw_pre"},
+                         {dmod_scale, nb, "dmod_scale"}, {dmod_shift, nb, "dmod_shift"},
+                         {ws, need, "the workspace"}};
+  LA_TRY(check_apart(outs, ins));
+  for (const Buffer& o : outs)
+    for (const void* in : {dh, dy})
+      if (!((o.p == dx || o.p == df) && o.p == in) && overlap(o.p, o.n, in, n))
+        return fail(LA_ERR_INVALID_ARG, "%s overlaps dh or dy without being it", o.name);
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (!any) {  // no rows: parameters that exist all the same get zeros
+    const Buffer zero[] = {{dgate, nb, ""}, {dw_post, nc, ""}, {dw_pre, nc, ""},
+                           {dmod_scale, nb, ""}, {dmod_shift, nb, ""}};
+    for (const Buffer& z : zero)
+      if (z.p != nullptr && z.n != 0) {
+        const cudaError_t e = cudaMemsetAsync(const_cast<void*>(z.p), 0, z.n, st);
+        if (e != cudaSuccess) return cuda_fail(e, "gated residual norm backward (no rows)");
+      }
+    return LA_OK;
+  }
+  const cudaError_t e = launch_norm_backward(
+      p, x, f, NormParams{gate, w_post, w_pre, mod_scale, nullptr}, dh, dy, dx, df,
+      NormGrads{dgate, dw_post, dw_pre, dmod_scale, dmod_shift}, static_cast<float*>(ws), st);
+  if (e != cudaSuccess) return cuda_fail(e, "gated residual norm backward");
   return LA_OK;
 }
 

@@ -46,4 +46,26 @@ struct RotaryProblem {
 cudaError_t launch_rotary(const RotaryProblem& p, const void* Q, const void* K, const int* pos,
                           void* Qo, void* Ko, cudaStream_t s);
 
+// Gated residual with the norms around it (la_norm.cu).
+constexpr int kNormMaxC = 8192;
+struct NormProblem {
+  int B, N, C;
+  int io, layer;   // layer: subtract the mean
+  float eps, alpha;
+  int ctas;        // backward: CTAs (and partial column sums) of a batch element
+};
+struct NormParams {  // [B, C] or [C] float32, or null
+  const float *gate, *w_post, *w_pre, *mod_scale, *mod_shift;
+};
+struct NormGrads {
+  float *gate, *w_post, *w_pre, *mod_scale, *mod_shift;
+};
+void norm_split(NormProblem& p);
+size_t norm_workspace_floats(const NormProblem& p);
+cudaError_t launch_norm(const NormProblem& p, const void* x, const void* f, const NormParams& w,
+                        void* h, void* y, cudaStream_t s);
+cudaError_t launch_norm_backward(const NormProblem& p, const void* x, const void* f,
+                                 const NormParams& w, const void* dh, const void* dy, void* dx,
+                                 void* df, const NormGrads& g, float* ws, cudaStream_t s);
+
 }  // namespace la

@@ -38,3 +38,4 @@ from .gated import (  # noqa: F401,E402
     gated_magnitudes,
 )
 from .rotary import rotary, rotary_rates  # noqa: F401,E402
+from .norm import gate_residual_norm, gate_residual_norm_backward  # noqa: F401,E402
