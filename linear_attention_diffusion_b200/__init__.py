@@ -461,60 +461,72 @@ def qkv_state(X, W, bias=None, rope_grid=None, t_offset: int = 0, rope_base: flo
 # wrappers check every tensor, run on the tensors' own device (on its current
 # stream unless one is given) and take their workspace from torch's allocator.
 
-def _io_of(x, name: str) -> str:
+def _io_of(x, name: str) -> int:
     import torch
-    if x.dtype == torch.bfloat16:
-        return "bf16"
-    if x.dtype == torch.float32:
-        return "f32"
+    if x.dtype is torch.bfloat16:
+        return LA_IO_BF16
+    if x.dtype is torch.float32:
+        return LA_IO_F32
     raise ValueError(f"{name} must be bfloat16 or float32, got {x.dtype}")
 
 
-def _need(name: str, x, shape, dtype, device) -> None:
+def _need(name: str, x, shape, dtype, device: int) -> None:
     """Raise ValueError unless x (None is left to the caller) is a contiguous tensor of this
-    shape, type and device."""
+    shape and type on GPU ``device`` (-1: the CPU)."""
     if x is None:
         return
-    if x.device != device or x.dtype != dtype or x.shape != shape or not x.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on {device}, got "
+    if x.dtype is not dtype or x.get_device() != device or x.shape != shape or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on GPU {device}, got "
                          f"{x.dtype} {tuple(x.shape)} with strides {x.stride()} on {x.device}")
 
 
-class _On:
-    """The tensors' device as the current one, and the stream to launch on."""
-
-    def __init__(self, device, stream):
-        import torch
-        if device.type != "cuda":
-            raise ValueError("tensor arguments must live on a CUDA device")
-        self._guard = None
-        if device.index != torch.cuda.current_device():
-            self._guard = torch.cuda.device(device)
-        self.stream = torch.cuda.current_stream(device).cuda_stream if stream is None else stream
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
-        return False
+def _at(x) -> Optional[int]:
+    """Address of a tensor that _need has seen."""
+    return None if x is None else x.data_ptr()
 
 
-def _gated_checks(Q, K, V, G, **states):
+def _launch(func, name: str, shape, args, device: int, stream) -> None:
+    """Call a C function on the tensors' own GPU and, unless one is given, its current stream."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    if not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if device == torch.cuda.current_device():
+        status = func(ctypes.byref(shape), *args, stream)
+    else:
+        with torch.cuda.device(device):
+            status = func(ctypes.byref(shape), *args, stream)
+    if status != LA_OK:
+        raise LaError(status, name)
+
+
+def _on_gpu(x) -> int:
+    if not x.is_cuda:
+        raise ValueError("tensor arguments must live on a CUDA device")
+    return x.get_device()
+
+
+def _scratch(nbytes: int, x):
+    """A workspace from torch's allocator and its size."""
+    import torch
+    return torch.empty(nbytes, dtype=torch.uint8, device=x.device), nbytes
+
+
+def _gated_shape(Q, K, V, G, scale, **states) -> LaGatedShape:
     import torch
     if Q.dim() != 4 or Q.shape[-1] != HEAD_DIM:
         raise ValueError(f"Q must be [B, N, H, {HEAD_DIM}], got {tuple(Q.shape)}")
     io = _io_of(Q, "Q")
-    B, N, H, D = Q.shape
-    for name, x in (("Q", Q), ("K", K), ("V", V)):
-        _need(name, x, Q.shape, Q.dtype, Q.device)
-    _need("G", G, (B, N, H), torch.float32, Q.device)
+    full, device = Q.shape, Q.get_device()
+    B, N, H, D = full
+    _need("Q", Q, full, Q.dtype, device)
+    _need("K", K, full, Q.dtype, device)
+    _need("V", V, full, Q.dtype, device)
+    _need("G", G, (B, N, H), torch.float32, device)
     for name, x in states.items():
-        _need(name, x, (B, H, D, D), torch.float32, Q.device)
-    return io
+        _need(name, x, (B, H, D, D), torch.float32, device)
+    return LaGatedShape(B, N, H, D, io, scale)
 
 
 def gated_attention(Q, K, V, G, S_in=None, scale: float = 1.0, want_state: bool = False, S_out=None,
@@ -523,15 +535,17 @@ def gated_attention(Q, K, V, G, S_in=None, scale: float = 1.0, want_state: bool 
     S_n = exp(g_n) S_{n-1} + k_n^T v_n, o_n = scale q_n S_n, for [B, N, H, 32] CUDA tensors and
     log gates G [B, N, H] float32. ``S_out`` may be ``S_in``: the state is then updated in place."""
     import torch
-    io = _gated_checks(Q, K, V, G, S_in=S_in, S_out=S_out)
-    B, N, H, D = Q.shape
-    shape = LaGatedShape(B, N, H, D, LA_IO_BF16 if io == "bf16" else LA_IO_F32, scale)
-    with _On(Q.device, stream) as st:
-        O = torch.empty_like(Q)
-        if S_out is None and want_state:
-            S_out = torch.empty((B, H, D, D), dtype=torch.float32, device=Q.device)
-        ws = torch.empty(la_gated_workspace_bytes(shape), dtype=torch.uint8, device=Q.device)
-        la_gated_attention(shape, Q, K, V, G, S_in, S_out, O, ws, st)
+    shape = _gated_shape(Q, K, V, G, scale, S_in=S_in, S_out=S_out)
+    device = _on_gpu(Q)
+    O = torch.empty_like(Q)
+    if S_out is None and want_state:
+        S_out = torch.empty((shape.B, shape.H, HEAD_DIM, HEAD_DIM), dtype=torch.float32, device=Q.device)
+    n = _lib.la_gated_workspace_bytes(ctypes.byref(shape), 0)
+    # 256: what a call that needs none reports
+    ws, n = _scratch(n, Q) if n > 256 else (None, 0)
+    _launch(_lib.la_gated_attention, "la_gated_attention", shape,
+            (Q.data_ptr(), K.data_ptr(), V.data_ptr(), G.data_ptr(), _at(S_in), _at(S_out), O.data_ptr(),
+             _at(ws), n), device, stream)
     return O if S_out is None else (O, S_out)
 
 
@@ -540,17 +554,19 @@ def gated_attention_backward(Q, K, V, G, dO, S_in=None, dS_out=None, scale: floa
     """dQ, dK, dV, dG, dS_in of gated_attention. dS_in is None unless ``want_state`` (by default:
     where an S_in is given); S_in must still hold the state that the forward began with."""
     import torch
-    io = _gated_checks(Q, K, V, G, S_in=S_in, dS_out=dS_out)
-    _need("dO", dO, Q.shape, Q.dtype, Q.device)
-    B, N, H, D = Q.shape
-    shape = LaGatedShape(B, N, H, D, LA_IO_BF16 if io == "bf16" else LA_IO_F32, scale)
+    shape = _gated_shape(Q, K, V, G, scale, S_in=S_in, dS_out=dS_out)
+    _need("dO", dO, Q.shape, Q.dtype, Q.get_device())
+    device = _on_gpu(Q)
     if want_state is None:
         want_state = S_in is not None
-    with _On(Q.device, stream) as st:
-        dQ, dK, dV, dG = (torch.empty_like(x) for x in (Q, K, V, G))
-        dS = torch.empty((B, H, D, D), dtype=torch.float32, device=Q.device) if want_state else None
-        ws = torch.empty(la_gated_workspace_bytes(shape, True), dtype=torch.uint8, device=Q.device)
-        la_gated_attention_backward(shape, Q, K, V, G, S_in, dO, dS_out, dQ, dK, dV, dG, dS, ws, st)
+    dQ, dK, dV, dG = (torch.empty_like(x) for x in (Q, K, V, G))
+    dS = None
+    if want_state:
+        dS = torch.empty((shape.B, shape.H, HEAD_DIM, HEAD_DIM), dtype=torch.float32, device=Q.device)
+    ws, n = _scratch(_lib.la_gated_workspace_bytes(ctypes.byref(shape), 1), Q)
+    _launch(_lib.la_gated_attention_backward, "la_gated_attention_backward", shape,
+            (Q.data_ptr(), K.data_ptr(), V.data_ptr(), G.data_ptr(), _at(S_in), dO.data_ptr(), _at(dS_out),
+             dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), dG.data_ptr(), _at(dS), _at(ws), n), device, stream)
     return dQ, dK, dV, dG, dS
 
 
@@ -588,43 +604,54 @@ def rotary(Q, K=None, positions=None, offset: int = 0, rot: Optional[int] = None
     if Q.dim() != 4:
         raise ValueError(f"Q must be [B, N, H, D], got {tuple(Q.shape)}")
     B, N, H, D = Q.shape
-    io = _io_of(Q, "Q")
-    _need("Q", Q, Q.shape, Q.dtype, Q.device)
+    io = "bf16" if _io_of(Q, "Q") == LA_IO_BF16 else "f32"
+    device = Q.get_device()
+    _need("Q", Q, Q.shape, Q.dtype, device)
     Hk = 0
     if K is not None:
         if K.dim() != 4:
             raise ValueError(f"K must be [B, N, Hk, D], got {tuple(K.shape)}")
         Hk = K.shape[2]
-        _need("K", K, (B, N, Hk, D), Q.dtype, Q.device)
+        _need("K", K, (B, N, Hk, D), Q.dtype, device)
     rows = positions is not None and positions.dim() == 2
-    _need("positions", positions, (B, N) if rows else (N,), torch.int32, Q.device)
+    _need("positions", positions, (B, N) if rows else (N,), torch.int32, device)
     Qo, Ko = (None, None) if out is None else out
-    _need("out[0]", Qo, Q.shape, Q.dtype, Q.device)
-    _need("out[1]", Ko, (B, N, Hk, D), Q.dtype, Q.device)
+    _need("out[0]", Qo, Q.shape, Q.dtype, device)
+    _need("out[1]", Ko, (B, N, Hk, D), Q.dtype, device)
     shape = make_rotary_shape(B, N, H, Hk, D, io, rot, layout, base, scaling, mscale, inverse, rows,
                               offset)
-    with _On(Q.device, stream) as st:
-        if Qo is None:
-            Qo = torch.empty_like(Q)
-        if Ko is None and K is not None:
-            Ko = torch.empty_like(K)
-        la_rotary(shape, Q, K, positions, Qo, Ko if K is not None else None, st)
-    return Qo, (Ko if K is not None else None)
+    device = _on_gpu(Q)
+    if Qo is None:
+        Qo = torch.empty_like(Q)
+    if K is None:
+        Ko = None
+    elif Ko is None:
+        Ko = torch.empty_like(K)
+    _launch(_lib.la_rotary, "la_rotary", shape,
+            (Q.data_ptr(), _at(K), _at(positions), Qo.data_ptr(), _at(Ko)), device, stream)
+    return Qo, Ko
 
 
-def _norm_checks(x, f, gate, w_post, w_pre, mod_scale, mod_shift, **like_x):
+_NORMS = {"rms": 0, "layer": 1}
+
+
+def _norm_shape(x, f, gate, w_post, w_pre, mod_scale, mod_shift, norm, eps, alpha, **like_x):
     import torch
     if x.dim() != 3:
         raise ValueError(f"x must be [B, N, C], got {tuple(x.shape)}")
     io = _io_of(x, "x")
-    B, _, C = x.shape
-    for name, t in (("x", x), ("f", f), *like_x.items()):
-        _need(name, t, x.shape, x.dtype, x.device)
-    for name, t in (("gate", gate), ("mod_scale", mod_scale), ("mod_shift", mod_shift)):
-        _need(name, t, (B, C), torch.float32, x.device)
-    for name, t in (("w_post", w_post), ("w_pre", w_pre)):
-        _need(name, t, (C,), torch.float32, x.device)
-    return io
+    full, device = x.shape, x.get_device()
+    B, N, C = full
+    _need("x", x, full, x.dtype, device)
+    _need("f", f, full, x.dtype, device)
+    for name, t in like_x.items():
+        _need(name, t, full, x.dtype, device)
+    _need("gate", gate, (B, C), torch.float32, device)
+    _need("mod_scale", mod_scale, (B, C), torch.float32, device)
+    _need("mod_shift", mod_shift, (B, C), torch.float32, device)
+    _need("w_post", w_post, (C,), torch.float32, device)
+    _need("w_pre", w_pre, (C,), torch.float32, device)
+    return LaNormShape(B, N, C, io, _NORMS[norm], eps, alpha)
 
 
 def gate_residual_norm(x, f=None, gate=None, w_post=None, w_pre=None, mod_scale=None, mod_shift=None,
@@ -639,14 +666,15 @@ def gate_residual_norm(x, f=None, gate=None, w_post=None, w_pre=None, mod_scale=
     may be x or f."""
     import torch
     h, y = (None, None) if out is None else out
-    io = _norm_checks(x, f, gate, w_post, w_pre, mod_scale, mod_shift, h=h, y=y)
-    shape = make_norm_shape(*x.shape, io, norm, eps, alpha)
-    with _On(x.device, stream) as st:
-        if h is None and f is not None and want_h:
-            h = torch.empty_like(x)
-        if y is None and want_y:
-            y = torch.empty_like(x)
-        la_gate_residual_norm(shape, x, f, gate, w_post, w_pre, mod_scale, mod_shift, h, y, st)
+    shape = _norm_shape(x, f, gate, w_post, w_pre, mod_scale, mod_shift, norm, eps, alpha, h=h, y=y)
+    device = _on_gpu(x)
+    if h is None and f is not None and want_h:
+        h = torch.empty_like(x)
+    if y is None and want_y:
+        y = torch.empty_like(x)
+    _launch(_lib.la_gate_residual_norm, "la_gate_residual_norm", shape,
+            (x.data_ptr(), _at(f), _at(gate), _at(w_post), _at(w_pre), _at(mod_scale), _at(mod_shift),
+             _at(h), _at(y)), device, stream)
     return h, y
 
 
@@ -656,13 +684,12 @@ def gate_residual_norm_backward(x, f, dy, dh, gate=None, w_post=None, w_pre=None
     """dx, df, dgate, dw_post, dw_pre, dmod_scale, dmod_shift of gate_residual_norm: None for what
     was not given (dmod_shift with mod_shift). f, and one of dy and dh, may be None."""
     import torch
-    io = _norm_checks(x, f, gate, w_post, w_pre, mod_scale, mod_shift, dy=dy, dh=dh)
-    shape = make_norm_shape(*x.shape, io, norm, eps, alpha)
-    with _On(x.device, stream) as st:
-        like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
-        dx, df, dgate, dwo, dwi, dsc, dsh = (like(t) for t in (x, f, gate, w_post, w_pre, mod_scale,
-                                                               mod_shift))
-        ws = torch.empty(la_norm_workspace_bytes(shape), dtype=torch.uint8, device=x.device)
-        la_gate_residual_norm_backward(shape, x, f, gate, w_post, w_pre, mod_scale, dh, dy, dx, df,
-                                       dgate, dwo, dwi, dsc, dsh, ws, st)
-    return dx, df, dgate, dwo, dwi, dsc, dsh
+    shape = _norm_shape(x, f, gate, w_post, w_pre, mod_scale, mod_shift, norm, eps, alpha, dy=dy, dh=dh)
+    device = _on_gpu(x)
+    grads = [None if t is None else torch.empty_like(t)
+             for t in (x, f, gate, w_post, w_pre, mod_scale, mod_shift)]
+    ws, n = _scratch(_lib.la_norm_workspace_bytes(ctypes.byref(shape)), x)
+    _launch(_lib.la_gate_residual_norm_backward, "la_gate_residual_norm_backward", shape,
+            (x.data_ptr(), _at(f), _at(gate), _at(w_post), _at(w_pre), _at(mod_scale), _at(dh), _at(dy),
+             *(_at(g) for g in grads), _at(ws), n), device, stream)
+    return tuple(grads)

@@ -73,28 +73,12 @@ struct Place {
   }
 };
 
-// The lane's piece of an output's next block.
-template <int NP>
-struct Out {
-  char* p;
-  ptrdiff_t down, block;  // bytes to the lane's next piece, to the next block
-  __device__ __forceinline__ Out(void* o, size_t base, size_t stride, int n0, int lane) {
-    using T = typename Io<NP>::T;
-    constexpr int kChunks = NP == 1 ? 4 : 8;
-    p = reinterpret_cast<char*>(static_cast<T*>(o) + base + (n0 + lane / kChunks) * stride) +
-        (lane % kChunks) * 16;
-    down = static_cast<ptrdiff_t>(TileLane<NP>::kRows * stride * sizeof(T));
-    block = static_cast<ptrdiff_t>(kGateBlock * stride * sizeof(T));
-  }
-};
-
 // Two bf16 blocks a step share one split of the state and one update, and fill the 32 lanes
 // with gates; float32 planes would not fit twice in shared memory beside enough warps.
 template <int NP>
 constexpr int kBlocks = NP == 1 ? 2 : 1;
 // Parts of what the kernels compute: two for a bf16 output, three for what ends in float32
-// (the gate's gradient is a difference of row sums) and for float32 tensors. The state's own
-// update always keeps 24 bits.
+// (the gate's gradient is a difference of row sums) and for float32 tensors.
 constexpr __host__ __device__ int parts(int NP, bool precise) { return NP == 1 && !precise ? 2 : 3; }
 
 // Products of one block row (16 tokens) with the tiles of its step, decayed and summed onto
@@ -144,7 +128,9 @@ __device__ __forceinline__ void block_row(float (&acc)[4][4], int b, const Frag<
 // One segment forwards. kBack = false: the forward itself, state rows = v's
 // dimensions. kBack = true: dq from (q, k, v) = (dO, V, K) with w = Q; it also
 // writes q . dq of every token and S at the anchors.
-template <int NP, bool kBack, int kStages>
+// kExact: the state's own update keeps 24 bits, for a state that goes out in float32 or stands
+// behind a float32 gradient; else 17, as many as a bf16 output can show.
+template <int NP, bool kBack, bool kExact, int kStages>
 __global__ void __launch_bounds__(kWarps * 32, 3) walk_kernel(const Walk a) {
   using T = typename Io<NP>::T;
   constexpr int NB = kBlocks<NP>, NT = kBack ? 4 : 3, NC = parts(NP, kBack);
@@ -167,8 +153,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) walk_kernel(const Walk a) {
                                                   at.n_begin, at.n_end, at.iters, lane);
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) ring.issue(lane);
-  const TileLane<NP> tl(lane);
-  Out<NP> out(a.o, at.base, at.stride, at.n_begin, lane);
+  Out<NP> out(a.o, at.base, p.H, at.n_begin, lane);
 
   State S;
   if (p.nseg > 1)
@@ -206,60 +191,72 @@ __global__ void __launch_bounds__(kWarps * 32, 3) walk_kernel(const Walk a) {
       S.store(anchors + static_cast<size_t>((n0 - at.n_begin) / a.anchor) * 1024, lane);
 
     const Decay<NP, NB> d(gate, lane);
-    const float head = d.head(lane), tail = d.tail(lane), whole = d.whole(lane);
-    // decays of the step's blocks, from its start and to its end
-    const float w0 = __shfl_sync(0xffffffffu, whole, 0);
-    const float w1 = NB == 1 ? 1.0f : __shfl_sync(0xffffffffu, whole, 16);
-    const float from_start = (NB == 2 && lane >= 16 ? head * w0 : head) * p.scale;
-    float acc[NB][4][4];
-    Frag<NP> q[NB];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) q[b].rows(tile[0] + b * kPlane, plane, off);
-    S.template apply<NP, NC, NB>(acc, q);
-    auto rest = [&](auto hard) {
-      constexpr bool kHard = decltype(hard)::value;
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        float r[2];
-        Decay<NP, NB>::spread_rows(from_start, b, lane, r);
-        scale_row<kHard>(acc[b], 0, r[0]);
-        scale_row<kHard>(acc[b], 1, r[1]);
-        block_row<NP, NB, NC, true, kHard>(acc[b], b, q[b], tile[1], tile[2], plane, off, d, head,
-                                           tail, p.scale, lane);
-      }
-    };
-    if (d.hard)
-      rest(Const<true>());
-    else
-      rest(Const<false>());
-    {
+    const int left = at.n_end - n0;
+    auto step = [&](auto careful) {
+      constexpr bool kHard = decltype(careful)::value;
+      const float head = d.template head<kHard>(lane), tail = d.template tail<kHard>(lane);
+      const float whole = d.template whole<kHard>(lane);
+      // decays of the step's blocks, from its start and to its end
+      const float w0 = __shfl_sync(0xffffffffu, whole, 0);
+      const float w1 = NB == 1 ? 1.0f : __shfl_sync(0xffffffffu, whole, 16);
+      const float from_start = (NB == 2 && lane >= 16 ? head * w0 : head) * p.scale;
       const float to_end = NB == 2 && lane < 16 ? tail * w1 : tail;
-      float wt[NB][4];
-      Frag<NP> v[NB], k[NB];
+      float acc[NB][4][4];
+      {
+        Frag<NP> q[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) q[b].rows(tile[0] + b * kPlane, plane, off);
+        S.template apply<NP, NC, NB>(acc, q);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          float r[2];
+          Decay<NP, NB>::spread_rows(from_start, b, lane, r);
+          scale_row<kHard>(acc[b], 0, r[0]);
+          scale_row<kHard>(acc[b], 1, r[1]);
+          block_row<NP, NB, NC, true, kHard>(acc[b], b, q[b], tile[1], tile[2], plane, off, d, head,
+                                             tail, p.scale, lane);
+        }
+      }
+      {
+        float wt[NB][4];
+        Frag<NP> v[NB], k[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          Decay<NP, NB>::spread(to_end, b, lane, wt[b]);
+          v[b].deep(tile[2] + b * kPlane, plane, off);
+          k[b].deep(tile[1] + b * kPlane, plane, off);
+        }
+        S.template update<NP, NB, kExact ? 3 : 2, kHard>(w0 * w1, v, k, wt);
+      }
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        Decay<NP, NB>::spread(to_end, b, lane, wt[b]);
-        v[b].deep(tile[2] + b * kPlane, plane, off);
-        k[b].deep(tile[1] + b * kPlane, plane, off);
-      }
-      S.template update<NP, NB>(w0 * w1, v, k, wt);
-    }
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const int left = at.n_end - n0 - b * kGateBlock;
-      if (kBack) {
-        float dots[2];
-        row_dots<NP>(acc[b], st + 3 * M::kTile + b * M::kTile / NB, tl, dots);
-        if ((lane & 3) == 0) {
-          float* r = a.rows + static_cast<size_t>(at.bh) * p.N + n0 + b * kGateBlock + r0;
-          if (r0 < left) r[0] = dots[0];
-          if (r0 + 8 < left) r[8] = dots[1];
+        if (kBack) {
+          float dots[2];
+          const uint32_t w = st + 3 * M::kTile + b * M::kTile / NB;
+          if constexpr (NP == 1) {
+            Frag<1> x;
+            x.rows(w, 0, off);
+            row_dots(acc[b], x, dots);
+          } else {
+            row_dots_f32(acc[b], w, lane, dots);
+          }
+          if ((lane & 3) == 0) {
+            float* r = a.rows + static_cast<size_t>(at.bh) * p.N + n0 + b * kGateBlock + r0;
+            if (!kHard || r0 + b * kGateBlock < left) r[0] = dots[0];
+            if (!kHard || r0 + b * kGateBlock + 8 < left) r[8] = dots[1];
+          }
         }
       }
       __syncwarp();  // every lane is done with the first tile: the output passes through it
-      store_tile<NP>(acc[b], st + b * M::kTile / NB, tl, out.p + b * out.block, out.down, left, lane);
-    }
-    out.p += NB * out.block;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) Out<NP>::put(acc[b], st + b * M::kTile / NB, off, lane);
+      __syncwarp();
+      out.template flush<kStep, !kHard>(st, left, kStep, lane);
+    };
+    if (d.hard || left < kStep)
+      step(Const<true>());
+    else
+      step(Const<false>());
   }
   cp_wait<0>();
   if (at.seg == p.nseg - 1) {
@@ -296,8 +293,7 @@ __global__ void __launch_bounds__(kWarps * 32, NP == 3 ? 2 : 3) walk_back_kernel
                                                  at.n_end, at.iters, lane);
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) ring.issue(lane);
-  const TileLane<NP> tl(lane);
-  Out<NP> out_k(a.o, at.base, at.stride, n0, lane), out_v(a.o2, at.base, at.stride, n0, lane);
+  Out<NP> out_k(a.o, at.base, p.H, n0, lane), out_v(a.o2, at.base, p.H, n0, lane);
 
   State X;
   if (p.nseg > 1)
@@ -337,72 +333,72 @@ __global__ void __launch_bounds__(kWarps * 32, NP == 3 ? 2 : 3) walk_back_kernel
       __syncwarp();
     }
     const Decay<NP, NB> d(gate, lane);
-    const float head = d.head(lane), tail = d.tail(lane), whole = d.whole(lane);
-    const float w0 = __shfl_sync(0xffffffffu, whole, 0);
-    const float w1 = NB == 1 ? 1.0f : __shfl_sync(0xffffffffu, whole, 16);
-    const float to_end = NB == 2 && lane < 16 ? tail * w1 : tail;
-    float kdots[NB][2];
-    // dk (which = 0): rows v, columns dO, summed over q; dv: rows k, columns q, summed over dO
+    const int left = at.n_end - n0;
+    auto step = [&](auto careful) {
+      constexpr bool kHard = decltype(careful)::value;
+      const float head = d.template head<kHard>(lane), tail = d.template tail<kHard>(lane);
+      const float whole = d.template whole<kHard>(lane);
+      const float w0 = __shfl_sync(0xffffffffu, whole, 0);
+      const float w1 = NB == 1 ? 1.0f : __shfl_sync(0xffffffffu, whole, 16);
+      const float to_end = NB == 2 && lane < 16 ? tail * w1 : tail;
+      const float from_start = (NB == 2 && lane >= 16 ? head * w0 : head) * p.scale;
+      float kdots[NB][2];
+      // dk (which = 0): rows v, columns dO, summed over q; dv: rows k, columns q, summed over
+      // dO. dk passes through v's tile, which is done with, dv then through k's.
+      auto side = [&](auto second) {
+        constexpr int which = decltype(second)::value;
+        float acc[NB][4][4];
+        Frag<NP> x[NB];
 #pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      float acc[NB][4][4];
-      Frag<NP> x[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) x[b].rows(tile[1 - which] + b * kPlane, plane, off);
-      if (which == 0)
-        X.template apply<NP, NK, NB>(acc, x);
-      else
-        X.template apply_turned<NP, NV, NB>(acc, x);
-      auto rest = [&](auto hard) {
-        constexpr bool kHard = decltype(hard)::value;
+        for (int b = 0; b < NB; ++b) x[b].rows(tile[1 - which] + b * kPlane, plane, off);
+        if (which == 0)
+          X.template apply<NP, NK, NB>(acc, x);
+        else
+          X.template apply_turned<NP, NV, NB>(acc, x);
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           float r[2];
           Decay<NP, NB>::spread_rows(to_end, b, lane, r);
           scale_row<kHard>(acc[b], 0, r[0]);
           scale_row<kHard>(acc[b], 1, r[1]);
-          if (which == 0)
-            block_row<NP, NB, NK, false, kHard>(acc[b], b, x[b], tile[3], tile[2], plane, off, d,
-                                                head, tail, p.scale, lane);
-          else
-            block_row<NP, NB, NV, false, kHard>(acc[b], b, x[b], tile[2], tile[3], plane, off, d,
-                                                head, tail, p.scale, lane);
+          block_row<NP, NB, which == 0 ? NK : NV, false, kHard>(
+              acc[b], b, x[b], tile[3 - which], tile[2 + which], plane, off, d, head, tail, p.scale,
+              lane);
         }
+        if (which == 0) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            if constexpr (NP == 1) {
+              Frag<1> k;
+              k.rows(tile[0] + b * kPlane, 0, off);
+              row_dots(acc[b], k, kdots[b]);
+            } else {
+              row_dots_f32(acc[b], st + b * M::kTile / NB, lane, kdots[b]);
+            }
+          }
+        }
+        const uint32_t pass = st + (1 - which) * M::kTile;
+        __syncwarp();
+#pragma unroll
+        for (int b = 0; b < NB; ++b) Out<NP>::put(acc[b], pass + b * M::kTile / NB, off, lane);
+        __syncwarp();
+        (which == 0 ? out_k : out_v).template flush<kStep, !kHard>(pass, left, -kStep, lane);
       };
-      if (d.hard)
-        rest(Const<true>());
-      else
-        rest(Const<false>());
-      if (which == 0) {
-        // k's own tile is still needed: dk waits in the registers of v's, which is not
+      side(Const<false>());
+      side(Const<true>());
+      {
+        float wt[NB][4];
+        Frag<NP> q[NB], o[NB];
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-          row_dots<NP>(acc[b], st + b * M::kTile / NB, tl, kdots[b]);
+        for (int b = 0; b < NB; ++b) {
+          Decay<NP, NB>::spread(from_start, b, lane, wt[b]);
+          q[b].deep(tile[2] + b * kPlane, plane, off);
+          o[b].deep(tile[3] + b * kPlane, plane, off);
+        }
+        X.template update<NP, NB, 3, kHard>(w0 * w1, q, o, wt);
       }
-      __syncwarp();  // v's (then k's) tile has been read: the output passes through it
-#pragma unroll
-      for (int b = 0; b < NB; ++b)
-        store_tile<NP>(acc[b], st + (1 - which) * M::kTile + b * M::kTile / NB, tl,
-                       (which == 0 ? out_k : out_v).p + b * out_k.block, out_k.down,
-                       at.n_end - n0 - b * kGateBlock, lane);
-    }
-    out_k.p -= NB * out_k.block;
-    out_v.p -= NB * out_k.block;
-    {
-      const float from_start = (NB == 2 && lane >= 16 ? head * w0 : head) * p.scale;
-      float wt[NB][4];
-      Frag<NP> q[NB], o[NB];
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        Decay<NP, NB>::spread(from_start, b, lane, wt[b]);
-        q[b].deep(tile[2] + b * kPlane, plane, off);
-        o[b].deep(tile[3] + b * kPlane, plane, off);
-      }
-      X.template update<NP, NB>(w0 * w1, q, o, wt);
-    }
-    // dg_t = dg_{t+1} + q_t . dq_t - k_t . dk_t, summed from the step's end; a stop
-    // passes no gradient and restarts the sum
-    {
+      // dg_t = dg_{t+1} + q_t . dq_t - k_t . dk_t, summed from the step's end; a stop
+      // passes no gradient and restarts the sum
       const int i = lane & (kStep - 1);
       float own = 0.0f;
 #pragma unroll
@@ -419,16 +415,20 @@ __global__ void __launch_bounds__(kWarps * 32, NP == 3 ? 2 : 3) walk_back_kernel
         if (i + s < kStep) x += y;
       }
       float dg = carry + x;
-      if (d.stops != 0) {
-        const uint32_t after = i == 31 ? 0u : d.stops & ~((2u << i) - 1u);
+      if (kHard && d.stops != 0) {
+        const uint32_t after = d.stops & ~((2u << i) - 1u);
         const float cut = __shfl_sync(0xffffffffu, x, after != 0 ? __ffs(after) - 1 : 0);
         if (after != 0) dg = x - cut;
         if ((d.stops >> i) & 1u) dg = 0.0f;
       }
-      if (lane < kStep && n0 + i < at.n_end)
+      if (lane < kStep && (!kHard || i < left))
         a.dG[at.gbase + static_cast<size_t>(n0 + i) * p.H] = dg;
       carry = __shfl_sync(0xffffffffu, dg, 0);
-    }
+    };
+    if (d.hard || left < kStep)
+      step(Const<true>());
+    else
+      step(Const<false>());
     if ((n0 - at.n_begin) % a.anchor == 0 && it + 1 < at.iters) {
       State S;
       S.load(anchors + static_cast<size_t>((n0 - at.n_begin) / a.anchor) * 1024, lane);
@@ -443,11 +443,15 @@ __global__ void __launch_bounds__(kWarps * 32, NP == 3 ? 2 : 3) walk_back_kernel
 // Every segment's own state from zero and its whole decay. Forward: S only, rows =
 // v's dimensions. Backward: S and X = sum_i (decay from the segment's start to i)
 // scale q_i^T dO_i, rows = k's (q's) dimensions. Segment s's S goes to slot s + 1 of
-// `states` (it becomes the state at the start of s + 1), its X to slot s - 1 of `grads`.
+// `states` (it becomes the state at the start of s + 1; the last one is the end of the row),
+// its X to slot s - 1 of `grads`. It walks a segment from its end: what it reads last, the
+// segments' first tokens, the walk reads first, while it is still in L2. Once the decay to
+// the segment's end has become 0, no earlier token has a part in S.
 template <int NP, bool kBack, int kStages>
 __global__ void __launch_bounds__(kWarps * 32, NP == 1 && !kBack ? 4 : 3)
-segment_kernel(const GatedProblem p, const void* qv, const void* kv, const void* vv,
-               const void* dov, const float* Gv, float* states, float* grads, float* decays) {
+segment_kernel(const GatedProblem p, int segs, const void* qv, const void* kv, const void* vv,
+               const void* dov, const float* Gv, float* states, float* last_states, float* grads,
+               float* decays) {
   using T = typename Io<NP>::T;
   constexpr int NB = kBlocks<NP>, NT = kBack ? 4 : 2;
   constexpr int kStep = NB * kGateBlock;
@@ -455,7 +459,6 @@ segment_kernel(const GatedProblem p, const void* qv, const void* kv, const void*
   extern __shared__ __align__(128) uint8_t smem_all[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long unit = static_cast<long long>(blockIdx.x) * kWarps + warp;
-  const int segs = kBack ? p.nseg : p.nseg - 1;  // nothing follows the last one forwards
   if (unit >= static_cast<long long>(p.B) * p.H * segs) return;
   const Place<NB> at(p, unit);
   const T* heads[NT];
@@ -467,8 +470,9 @@ segment_kernel(const GatedProblem p, const void* qv, const void* kv, const void*
   }
   const uint32_t smem = smem_addr(smem_all) + warp * M::kWarp;
   const uint32_t planes = smem + kStages * M::kStage;
-  Ring<NP, NB, NT, kStages, NT, false, false> ring(smem, heads, Gv + at.gbase, p.H, nullptr,
-                                                   at.n_begin, at.n_end, at.iters, lane);
+  Ring<NP, NB, NT, kStages, NT, true, false> ring(smem, heads, Gv + at.gbase, p.H, nullptr,
+                                                  at.n_begin + (at.iters - 1) * kStep, at.n_end,
+                                                  at.iters, lane);
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) ring.issue(lane);
   State S, X;
@@ -494,40 +498,50 @@ segment_kernel(const GatedProblem p, const void* qv, const void* kv, const void*
       __syncwarp();
     }
     const Decay<NP, NB> d(gate, lane);
-    const float whole = d.whole(lane);
-    const float w0 = __shfl_sync(0xffffffffu, whole, 0);
-    const float w1 = NB == 1 ? 1.0f : __shfl_sync(0xffffffffu, whole, 16);
-    float w[NB][4];
-    {
-      const float tail = d.tail(lane);
-      const float to_end = NB == 2 && lane < 16 ? tail * w1 : tail;
-      Frag<NP> x[NB], y[NB];
+    auto step = [&](auto careful) {
+      constexpr bool kHard = decltype(careful)::value;
+      const float whole = d.template whole<kHard>(lane);
+      const float w0 = __shfl_sync(0xffffffffu, whole, 0);
+      const float w1 = NB == 1 ? 1.0f : __shfl_sync(0xffffffffu, whole, 16);
+      float w[NB][4];
+      if (!kBack || total != 0.0f) {
+        const float tail = d.template tail<kHard>(lane);
+        const float to_end = (NB == 2 && lane < 16 ? tail * w1 : tail) * total;
+        Frag<NP> x[NB], y[NB];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        Decay<NP, NB>::spread(to_end, b, lane, w[b]);
-        x[b].deep(tile[0] + b * kPlane, plane, off);
-        y[b].deep(tile[1] + b * kPlane, plane, off);
+        for (int b = 0; b < NB; ++b) {
+          Decay<NP, NB>::spread(to_end, b, lane, w[b]);
+          x[b].deep(tile[0] + b * kPlane, plane, off);
+          y[b].deep(tile[1] + b * kPlane, plane, off);
+        }
+        S.template update<NP, NB, 3, false>(1.0f, x, y, w);
       }
-      S.template update<NP, NB>(w0 * w1, x, y, w);
-    }
-    if (kBack) {
-      const float head = d.head(lane);
-      const float from_start =
-          (NB == 2 && lane >= 16 ? head * w0 : head) * (p.scale * total);
-      Frag<NP> x[NB], y[NB];
+      if (kBack) {
+        const float head = d.template head<kHard>(lane);
+        const float from_start = (NB == 2 && lane >= 16 ? head * w0 : head) * p.scale;
+        Frag<NP> x[NB], y[NB];
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        Decay<NP, NB>::spread(from_start, b, lane, w[b]);
-        x[b].deep(tile[2] + b * kPlane, plane, off);
-        y[b].deep(tile[3] + b * kPlane, plane, off);
+        for (int b = 0; b < NB; ++b) {
+          Decay<NP, NB>::spread(from_start, b, lane, w[b]);
+          x[b].deep(tile[NT - 2] + b * kPlane, plane, off);
+          y[b].deep(tile[NT - 1] + b * kPlane, plane, off);
+        }
+        X.template update<NP, NB, 3, kHard>(w0 * w1, x, y, w);
       }
-      X.template update<NP, NB>(1.0f, x, y, w);
-    }
-    total *= w0 * w1;
+      total *= w0 * w1;
+    };
+    if (d.hard)
+      step(Const<true>());
+    else
+      step(Const<false>());
+    if (!kBack && total == 0.0f) break;
   }
   cp_wait<0>();
   const size_t slots = static_cast<size_t>(at.bh) * p.nseg;
-  if (at.seg + 1 < p.nseg) S.store(states + (slots + at.seg + 1) * 1024, lane);
+  if (at.seg + 1 < p.nseg)
+    S.store(states + (slots + at.seg + 1) * 1024, lane);
+  else if (!kBack)
+    S.store(last_states + static_cast<size_t>(at.bh) * 1024, lane);
   if (kBack && at.seg > 0) X.store(grads + (slots + at.seg - 1) * 1024, lane);
   if (lane == 0) decays[slots + at.seg] = total;
 }
@@ -535,10 +549,11 @@ segment_kernel(const GatedProblem p, const void* qv, const void* kv, const void*
 // Segments in order: slot s becomes the state at segment s's start (forwards), or the
 // gradient at its end (backwards). One thread per four numbers of a head's state, 64 threads
 // a CTA so that few heads still spread over the SMs; blockIdx.z = 0: states, 1: gradients.
+// With s_final the states go on over the last segment, whose own state is in `tail_state`.
 template <bool kTransposed>
 __global__ void __launch_bounds__(64)
 combine_kernel(int nseg, const float* decays, float* states, const float* s_init, float* grads,
-               const float* x_init) {
+               const float* x_init, const float* tail_state, float* s_final) {
   const int bh = blockIdx.x, f = blockIdx.y * 64 + threadIdx.x;
   const bool back = blockIdx.z == 1;
   float4* slot = reinterpret_cast<float4*>(back ? grads : states) +
@@ -579,6 +594,18 @@ combine_kernel(int nseg, const float* decays, float* states, const float* s_init
         run.w = fmaf(m[k], run.w, t[k].w);
         slot[static_cast<size_t>(s) * 256] = run;
       }
+  }
+  if (s_final != nullptr) {
+    const float m = dec[nseg - 1];
+    const float4 t = __ldcg(reinterpret_cast<const float4*>(tail_state) +
+                            static_cast<size_t>(bh) * 256 + f);
+    if (m == 0.0f) run = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const int mt = f >> 7, nt = (f >> 5) & 3, lane = f & 31;
+    s_final += static_cast<size_t>(bh) * 1024;
+    s_final[State::outer<kTransposed>(mt, nt, 0, lane)] = fmaf(m, run.x, t.x);
+    s_final[State::outer<kTransposed>(mt, nt, 1, lane)] = fmaf(m, run.y, t.y);
+    s_final[State::outer<kTransposed>(mt, nt, 2, lane)] = fmaf(m, run.z, t.z);
+    s_final[State::outer<kTransposed>(mt, nt, 3, lane)] = fmaf(m, run.w, t.w);
   }
 }
 
@@ -680,17 +707,19 @@ cudaError_t forward(const GatedProblem& p, const void* Q, const void* K, const v
   constexpr int NB = kBlocks<NP>, kSegStages = 3, kStages = NP == 1 ? 3 : 2;
   const long long BH = 1LL * p.B * p.H;
   float* states = ws;
-  float* decays = ws + BH * p.nseg * 1024;
+  float* last_states = states + BH * p.nseg * 1024;
+  float* decays = last_states + BH * 1024;
   cudaError_t e;
   if (p.nseg > 1) {
     auto seg = segment_kernel<NP, false, kSegStages>;
     const int bytes = kWarps * Smem<NP, NB, 2, kSegStages>::kWarp;
     if ((e = allow_smem(seg, bytes)) != cudaSuccess) return e;
-    seg<<<grid_of(BH * (p.nseg - 1)), kWarps * 32, bytes, s>>>(p, Q, K, V, nullptr, G, states,
-                                                              nullptr, decays);
+    const int segs = S_out != nullptr ? p.nseg : p.nseg - 1;
+    seg<<<grid_of(BH * segs), kWarps * 32, bytes, s>>>(p, segs, Q, K, V, nullptr, G, states,
+                                                       last_states, nullptr, decays);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     combine_kernel<true><<<dim3(static_cast<unsigned>(BH), 4, 1), 64, 0, s>>>(
-        p.nseg, decays, states, S_in, nullptr, nullptr);
+        p.nseg, decays, states, S_in, nullptr, nullptr, last_states, S_out);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   Walk a = {};
@@ -700,10 +729,13 @@ cudaError_t forward(const GatedProblem& p, const void* Q, const void* K, const v
   a.G = G;
   a.o = O;
   a.init = S_in;
-  a.final_ = S_out;
+  a.final_ = p.nseg > 1 ? nullptr : S_out;
   a.prefix = states;
   a.p = p;
-  auto walk = walk_kernel<NP, false, kStages>;
+  auto walk = walk_kernel<NP, false, true, kStages>;
+  if constexpr (NP == 1) {
+    if (a.final_ == nullptr) walk = walk_kernel<NP, false, false, kStages>;
+  }
   const int bytes = kWarps * Smem<NP, NB, 3, kStages, 3>::kWarp;
   if ((e = allow_smem(walk, bytes)) != cudaSuccess) return e;
   walk<<<grid_of(BH * p.nseg), kWarps * 32, bytes, s>>>(a);
@@ -733,10 +765,11 @@ cudaError_t backward(const GatedProblem& p, const void* Q, const void* K, const 
     auto seg = segment_kernel<NP, true, kStages>;
     const int bytes = kWarps * Smem<NP, NB, 4, kStages>::kWarp;
     if ((e = allow_smem(seg, bytes)) != cudaSuccess) return e;
-    seg<<<grid_of(BH * p.nseg), kWarps * 32, bytes, s>>>(p, Q, K, V, dO, G, states, grads, decays);
+    seg<<<grid_of(BH * p.nseg), kWarps * 32, bytes, s>>>(p, p.nseg, Q, K, V, dO, G, states, nullptr,
+                                                         grads, decays);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     combine_kernel<false><<<dim3(static_cast<unsigned>(BH), 4, 2), 64, 0, s>>>(
-        p.nseg, decays, states, S_in, grads, dS_out);
+        p.nseg, decays, states, S_in, grads, dS_out, nullptr, nullptr);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   a.G = G;
@@ -748,7 +781,7 @@ cudaError_t backward(const GatedProblem& p, const void* Q, const void* K, const 
   a.o = dQ;
   a.init = S_in;
   a.prefix = states;
-  auto walk = walk_kernel<NP, true, kStages>;
+  auto walk = walk_kernel<NP, true, true, kStages>;
   int bytes = kWarps * Smem<NP, NB, 4, kStages, 3>::kWarp;
   if ((e = allow_smem(walk, bytes)) != cudaSuccess) return e;
   walk<<<grid_of(BH * p.nseg), kWarps * 32, bytes, s>>>(a);
@@ -789,7 +822,7 @@ void gated_split(GatedProblem& p) {
 size_t gated_workspace_floats(const GatedProblem& p, bool backward) {
   const size_t BH = static_cast<size_t>(p.B) * p.H;
   const size_t states = BH * p.nseg * 1024, decays = BH * p.nseg;
-  if (!backward) return p.nseg > 1 ? states + decays : 0;
+  if (!backward) return p.nseg > 1 ? states + BH * 1024 + decays : 0;
   const size_t anchors = BH * (static_cast<size_t>(p.nseg) * gated::gated_anchors(p) + 1) * 1024;
   return 2 * states + anchors + (BH * p.N + 3) / 4 * 4 + decays;
 }

@@ -70,6 +70,13 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
                : "r"(addr)
                : "memory");
 }
+// The store of the same layout: four 8x8 matrices, each lane one row's address.
+__device__ __forceinline__ void stsm4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c,
+                                      uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a),
+               "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -340,17 +347,18 @@ struct State {
 
   // state = decay * state + sum over the tokens of NB blocks of w A^T B; A gives the rows,
   // B the columns, w[b] the weights of tokens 2 (l % 4) + {0, 1, 8, 9} of block b.
-  template <int NP, int NB>
+  // The weighted numbers keep 24 bits (kParts = 3) or 17 (2).
+  template <int NP, int NB, int kParts, bool kHard>
   __device__ __forceinline__ void update(float decay, const Frag<NP> (&A)[NB],
                                          const Frag<NP> (&B)[NB], const float (&w)[NB][4]) {
-    constexpr int NC = NP == 1 ? 4 : 3;
-    if (decay == 0.0f) zero();  // the same in all lanes: a stop drops the state whatever it holds
-    uint32_t wp[NB][2][3];
+    constexpr int NC = NP == 1 && kParts == 3 ? 4 : kParts == 2 && NP == 1 ? 2 : 3;
+    if (kHard && decay == 0.0f) zero();  // a stop drops the state whatever it holds
+    uint32_t wp[NB][2][kParts];
     if (NP == 1) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        split2<3>(w[b][0], w[b][1], wp[b][0]);
-        split2<3>(w[b][2], w[b][3], wp[b][1]);
+        split2<kParts>(w[b][0], w[b][1], wp[b][0]);
+        split2<kParts>(w[b][2], w[b][3], wp[b][1]);
       }
     }
 #pragma unroll
@@ -364,14 +372,20 @@ struct State {
           if (NP == 1) {
             // w = w0 + w1 + w2 in bf16 parts: v w0 is exactly its rounding and one more bf16;
             // v w1 likewise, the latter with v w2 added. Packed arithmetic, five instructions
-            // for two numbers where a float32 product split three ways takes fifteen.
-            const uint32_t(&x)[3] = wp[b][i & 1];
+            // for two numbers where a float32 product split three ways takes fifteen. With two
+            // parts v w1 is added to what the rounding of v w0 left.
+            const uint32_t(&x)[kParts] = wp[b][i & 1];
             const uint32_t v = A[b].r[0][mt][i];
-            const uint32_t p0 = mul2(v, x[0]), p2 = mul2(v, x[1]);
+            const uint32_t p0 = mul2(v, x[0]), left = fma2(v, x[0], neg2(p0));
             a[b][0][at] = p0;
-            a[b][1][at] = fma2(v, x[0], neg2(p0));
-            a[b][NC - 2][at] = p2;
-            a[b][NC - 1][at] = fma2(v, x[2], fma2(v, x[1], neg2(p2)));
+            if (NC == 4) {
+              const uint32_t p2 = mul2(v, x[1]);
+              a[b][1][at] = left;
+              a[b][NC - 2][at] = p2;
+              a[b][NC - 1][at] = fma2(v, x[kParts - 1], fma2(v, x[1], neg2(p2)));
+            } else {
+              a[b][1][at] = fma2(v, x[1], left);
+            }
           } else {
             float f = 0.0f, g = 0.0f;
 #pragma unroll
@@ -524,14 +538,16 @@ __device__ __forceinline__ void scale_row(float (&acc)[4][4], int h, float f) {
 // A decay is the difference of two such sums. Where a sum passes kEasy in size (and always for
 // float32 tensors) the sums carry what their rounding left in `low`, so that gates of -100 do
 // not cost the small gates next to them their low bits; below it the difference is good to
-// 2^-19. Stops are minded only where there are any (`hard`). Each is one branch for the warp.
+// 2^-18. There, and where something stops, a step is `hard`: it runs a second copy of the
+// step's code that minds both, so that the ordinary one stays free of branches, one long
+// stretch in which the scheduler can lay products beside the arithmetic around them.
 template <int NP, int NB>
 struct Decay {
-  static constexpr float kEasy = NP == 1 ? -16.0f : 1.0f;
+  static constexpr float kEasy = NP == 1 ? -32.0f : 1.0f;
   float c, low;          // sum at the lane's token: c + low
   float last, last_low;  // the same at the last token of its block
   uint32_t stops;        // bit i: token i's gate lets nothing through
-  bool wide, hard;
+  bool hard;
   __device__ __forceinline__ Decay(float g, int lane) {
     float x = g * kLog2e;
     const bool stop = x < kStop;
@@ -546,8 +562,8 @@ struct Decay {
       if ((lane & 15) >= d) x += y;
     }
     c = x;
-    hard = stops != 0;
-    wide = NP > 1 || __any_sync(0xffffffffu, !(c >= kEasy));
+    const bool wide = NP > 1 || __any_sync(0xffffffffu, !(c >= kEasy));
+    hard = wide || stops != 0;
     if (wide) {
       x = x0;
 #pragma unroll
@@ -570,18 +586,21 @@ struct Decay {
     return NB == 1 ? stops : (stops >> (lane & 16)) & 0xffffu;
   }
   // from the state before the lane's block to its token
+  template <bool kHard>
   __device__ __forceinline__ float head(int lane) const {
     const float f = exp2_fast(c);
-    return hard && (own_stops(lane) & ((2u << (lane & 15)) - 1u)) ? 0.0f : f;
+    return kHard && (own_stops(lane) & ((2u << (lane & 15)) - 1u)) ? 0.0f : f;
   }
   // from the lane's token to its block's end
+  template <bool kHard>
   __device__ __forceinline__ float tail(int lane) const {
-    const float f = exp2_fast((last - c) + (last_low - low));
-    return hard && (own_stops(lane) >> ((lane & 15) + 1)) ? 0.0f : f;
+    const float f = exp2_fast(kHard ? (last - c) + (last_low - low) : last - c);
+    return kHard && (own_stops(lane) >> ((lane & 15) + 1)) ? 0.0f : f;
   }
   // over the whole of the lane's block
+  template <bool kHard>
   __device__ __forceinline__ float whole(int lane) const {
-    return own_stops(lane) ? 0.0f : exp2_fast(last);
+    return kHard && own_stops(lane) ? 0.0f : exp2_fast(last);
   }
   // of `x`, one value per token: the values of tokens 16 b + 2 (l % 4) + {0, 1, 8, 9}
   static __device__ __forceinline__ void spread(float x, int b, int lane, float (&out)[4]) {
@@ -606,7 +625,7 @@ struct Decay {
     float cc[4], cr[2], cl[4] = {0.0f, 0.0f, 0.0f, 0.0f}, lr[2] = {0.0f, 0.0f};
     spread(c, b, lane, cc);
     spread_rows(c, b, lane, cr);
-    if (wide) {
+    if (kHard) {
       spread(low, b, lane, cl);
       spread_rows(low, b, lane, lr);
     }
@@ -635,8 +654,8 @@ struct Decay {
           continue;
         }
         float d = kRowsLater ? cr[h] - cc[x] : cc[x] - cr[h];
-        if (wide) d += kRowsLater ? lr[h] - cl[x] : cl[x] - lr[h];
         if (kHard) {
+          d += kRowsLater ? lr[h] - cl[x] : cl[x] - lr[h];
           l[h][x] = col >= first && col < end ? exp2_fast(d) : 0.0f;
         } else {
           const float f = exp2_fast(d);
@@ -820,70 +839,84 @@ __device__ __forceinline__ void split_tile(uint32_t src, uint32_t planes, int la
   }
 }
 
-// Where a lane's accumulator numbers (rows l / 4 and + 8, columns 8 e + 2 (l % 4) and + 1) and
-// its 16-byte pieces of whole rows lie in a block's tile.
+// Rows of an output: an accumulator goes to a free tile in shared memory (put), and from there
+// in 16-byte pieces, four or eight lanes a row, to the tensor (flush, after a __syncwarp).
 template <int NP>
-struct TileLane {
-  uint32_t acc[NP == 1 ? 4 : 4];  // per e, row l / 4; 8 rows down: kDown
+struct Out {
+  static constexpr int kChunks = NP == 1 ? 4 : 8;  // of a row
+  static constexpr int kRows = 32 / kChunks;       // rows the warp stores at once
+  static constexpr int kRowBytes = NP == 1 ? 64 : 128;
+  char* p;       // the lane's first piece of the next block
+  int pitch;     // bytes of a token in the tensor
   uint32_t piece;
-  static constexpr int kDown = NP == 1 ? 512 : 1024;
-  static constexpr int kPieces = NP == 1 ? 2 : 4;   // of a lane
-  static constexpr int kRows = 16 / kPieces;        // rows between them
-  __device__ __forceinline__ explicit TileLane(int lane) {
-    const int r = lane >> 2, q = lane & 3;
+  __device__ __forceinline__ Out(void* o, size_t base, int heads, int n0, int lane) {
+    using T = typename Io<NP>::T;
+    pitch = heads * 32 * static_cast<int>(sizeof(T));
+    const int row = lane / kChunks, c = lane % kChunks;
+    p = reinterpret_cast<char*>(static_cast<T*>(o) + base) + static_cast<size_t>(n0 + row) * pitch +
+        c * 16;
+    piece = NP == 1 ? tile_off(row, c) : tile_off_f32(row, c);
+  }
+  static __device__ __forceinline__ void put(const float (&acc)[4][4], uint32_t tile,
+                                             const LaneOff& off, int lane) {
+    if (NP == 1) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      acc[e] = NP == 1 ? tile_off(r, e) + q * 4
-                       : tile_off_f32(r, 2 * e + (q >> 1)) + (q & 1) * 8;
-    piece = NP == 1 ? tile_off(lane >> 2, lane & 3) : tile_off_f32(lane >> 3, lane & 7);
+      for (int ks = 0; ks < 2; ++ks)
+        stsm4(tile + off.a[ks], pack2(acc[2 * ks][0], acc[2 * ks][1]),
+              pack2(acc[2 * ks][2], acc[2 * ks][3]), pack2(acc[2 * ks + 1][0], acc[2 * ks + 1][1]),
+              pack2(acc[2 * ks + 1][2], acc[2 * ks + 1][3]));
+    } else {
+      const int r = lane >> 2, q = lane & 3;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          sts2(tile + tile_off_f32(r + 8 * h, 2 * e + (q >> 1)) + (q & 1) * 8, acc[e][2 * h],
+               acc[e][2 * h + 1]);
+    }
+  }
+  // `tokens` of the tile at hand, of which `rows` exist; moves on by `step` tokens.
+  template <int kTokens, bool kWhole>
+  __device__ __forceinline__ void flush(uint32_t tile, int rows, int step, int lane) {
+    char* dst = p;
+    const int down = kRows * pitch;
+#pragma unroll
+    for (int i = 0; i < kTokens / kRows; ++i, dst += down) {
+      const uint4 v = lds4(tile + piece + i * kRows * kRowBytes);
+      if (kWhole || lane / kChunks + i * kRows < rows) *reinterpret_cast<uint4*>(dst) = v;
+    }
+    p += static_cast<ptrdiff_t>(step) * pitch;
   }
 };
 
-// acc (16 tokens x 32, accumulators) through shared memory to rows of the tensor; `dst` is the
-// lane's first piece, `down` the bytes to its next.
-template <int NP>
-__device__ __forceinline__ void store_tile(const float (&acc)[4][4], uint32_t tile,
-                                           const TileLane<NP>& tl, char* dst, ptrdiff_t down,
-                                           int rows, int lane) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (NP == 1)
-        sts(tile + tl.acc[e] + h * TileLane<NP>::kDown, pack2(acc[e][2 * h], acc[e][2 * h + 1]));
-      else
-        sts2(tile + tl.acc[e] + h * TileLane<NP>::kDown, acc[e][2 * h], acc[e][2 * h + 1]);
-    }
-  __syncwarp();
-  const int row = lane / (NP == 1 ? 4 : 8);
-#pragma unroll
-  for (int i = 0; i < TileLane<NP>::kPieces; ++i, dst += down) {
-    const uint4 v = lds4(tile + tl.piece + i * TileLane<NP>::kRows * (NP == 1 ? 64 : 128));
-    if (rows >= 16 || row + i * TileLane<NP>::kRows < rows) *reinterpret_cast<uint4*>(dst) = v;
-  }
-}
-
-// Sum over the 32 dimensions of acc * X, X the tile as it lies in shared memory
-// (bf16 or float32): the values of tokens l / 4 and l / 4 + 8, in every lane of the four.
-template <int NP>
-__device__ __forceinline__ void row_dots(const float (&acc)[4][4], uint32_t tile,
-                                         const TileLane<NP>& tl, float (&out)[2]) {
+// Sum over the 32 dimensions of acc * X for tokens l / 4 and l / 4 + 8, in every lane of the
+// four: bf16 from X as an operand (its numbers lie where an accumulator's do), float32 from
+// the tile as it lies in shared memory.
+__device__ __forceinline__ void row_dots(const float (&acc)[4][4], const Frag<1>& X,
+                                         float (&out)[2]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     float s = 0.0f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      float x, y;
-      if (NP == 1) {
-        const uint32_t v = __float_as_uint(lds(tile + tl.acc[e] + h * TileLane<NP>::kDown));
-        x = lo_f(v);
-        y = hi_f(v);
-      } else {
-        const uint2 v = lds2(tile + tl.acc[e] + h * TileLane<NP>::kDown);
-        x = __uint_as_float(v.x);
-        y = __uint_as_float(v.y);
-      }
-      s = fmaf(acc[e][2 * h], x, fmaf(acc[e][2 * h + 1], y, s));
+      const uint32_t v = X.r[0][e >> 1][2 * (e & 1) + h];
+      s = fmaf(acc[e][2 * h], lo_f(v), fmaf(acc[e][2 * h + 1], hi_f(v), s));
+    }
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    out[h] = s;
+  }
+}
+__device__ __forceinline__ void row_dots_f32(const float (&acc)[4][4], uint32_t tile, int lane,
+                                             float (&out)[2]) {
+  const int r = lane >> 2, q = lane & 3;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint2 v = lds2(tile + tile_off_f32(r + 8 * h, 2 * e + (q >> 1)) + (q & 1) * 8);
+      s = fmaf(acc[e][2 * h], __uint_as_float(v.x), fmaf(acc[e][2 * h + 1], __uint_as_float(v.y), s));
     }
     s += __shfl_xor_sync(0xffffffffu, s, 1);
     s += __shfl_xor_sync(0xffffffffu, s, 2);
