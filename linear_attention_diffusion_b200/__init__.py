@@ -461,8 +461,20 @@ def qkv_state(X, W, bias=None, rope_grid=None, t_offset: int = 0, rope_base: flo
 # wrappers check every tensor, run on the tensors' own device (on its current
 # stream unless one is given) and take their workspace from torch's allocator.
 
+_torch = None
+
+
+def _t():
+    """torch, imported at the first call that needs it."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _io_of(x, name: str) -> int:
-    import torch
+    torch = _t()
     if x.dtype is torch.bfloat16:
         return LA_IO_BF16
     if x.dtype is torch.float32:
@@ -487,10 +499,10 @@ def _at(x) -> Optional[int]:
 
 def _launch(func, name: str, shape, args, device: int, stream) -> None:
     """Call a C function on the tensors' own GPU and, unless one is given, its current stream."""
-    import torch
+    torch = _t()
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    if not isinstance(stream, int):
+        stream = torch.cuda.current_stream(device).cuda_stream
+    elif not isinstance(stream, int):
         stream = stream.cuda_stream
     if device == torch.cuda.current_device():
         status = func(ctypes.byref(shape), *args, stream)
@@ -509,12 +521,12 @@ def _on_gpu(x) -> int:
 
 def _scratch(nbytes: int, x):
     """A workspace from torch's allocator and its size."""
-    import torch
+    torch = _t()
     return torch.empty(nbytes, dtype=torch.uint8, device=x.device), nbytes
 
 
 def _gated_shape(Q, K, V, G, scale, **states) -> LaGatedShape:
-    import torch
+    torch = _t()
     if Q.dim() != 4 or Q.shape[-1] != HEAD_DIM:
         raise ValueError(f"Q must be [B, N, H, {HEAD_DIM}], got {tuple(Q.shape)}")
     io = _io_of(Q, "Q")
@@ -534,12 +546,12 @@ def gated_attention(Q, K, V, G, S_in=None, scale: float = 1.0, want_state: bool 
     """O (and the last state when ``want_state`` or ``S_out`` is given) of gated linear attention:
     S_n = exp(g_n) S_{n-1} + k_n^T v_n, o_n = scale q_n S_n, for [B, N, H, 32] CUDA tensors and
     log gates G [B, N, H] float32. ``S_out`` may be ``S_in``: the state is then updated in place."""
-    import torch
+    torch = _t()
     shape = _gated_shape(Q, K, V, G, scale, S_in=S_in, S_out=S_out)
     device = _on_gpu(Q)
     O = torch.empty_like(Q)
     if S_out is None and want_state:
-        S_out = torch.empty((shape.B, shape.H, HEAD_DIM, HEAD_DIM), dtype=torch.float32, device=Q.device)
+        S_out = G.new_empty((shape.B, shape.H, HEAD_DIM, HEAD_DIM)) if S_in is None else torch.empty_like(S_in)
     n = _lib.la_gated_workspace_bytes(ctypes.byref(shape), 0)
     # 256: what a call that needs none reports
     ws, n = _scratch(n, Q) if n > 256 else (None, 0)
@@ -553,7 +565,7 @@ def gated_attention_backward(Q, K, V, G, dO, S_in=None, dS_out=None, scale: floa
                              want_state: Optional[bool] = None, stream=None):
     """dQ, dK, dV, dG, dS_in of gated_attention. dS_in is None unless ``want_state`` (by default:
     where an S_in is given); S_in must still hold the state that the forward began with."""
-    import torch
+    torch = _t()
     shape = _gated_shape(Q, K, V, G, scale, S_in=S_in, dS_out=dS_out)
     _need("dO", dO, Q.shape, Q.dtype, Q.get_device())
     device = _on_gpu(Q)
@@ -600,7 +612,7 @@ def rotary(Q, K=None, positions=None, offset: int = 0, rot: Optional[int] = None
     ``positions``: int32 [N] or [B, N], or None for offset + n. ``rot``: dimensions that turn
     (default: all). ``inverse`` turns back, which is the gradient. ``out``: (Qo, Ko), which may be
     (Q, K) to work in place. Frequencies and ``scaling``: see make_rotary_shape and include/la.h."""
-    import torch
+    torch = _t()
     if Q.dim() != 4:
         raise ValueError(f"Q must be [B, N, H, D], got {tuple(Q.shape)}")
     B, N, H, D = Q.shape
@@ -636,7 +648,7 @@ _NORMS = {"rms": 0, "layer": 1}
 
 
 def _norm_shape(x, f, gate, w_post, w_pre, mod_scale, mod_shift, norm, eps, alpha, **like_x):
-    import torch
+    torch = _t()
     if x.dim() != 3:
         raise ValueError(f"x must be [B, N, C], got {tuple(x.shape)}")
     io = _io_of(x, "x")
@@ -664,7 +676,7 @@ def gate_residual_norm(x, f=None, gate=None, w_post=None, w_pre=None, mod_scale=
     with float32 parameters gate, mod_scale, mod_shift [B, C] and w_post, w_pre [C]. h is None
     without f or with ``want_h=False``, y with ``want_y=False``. ``out``: (h, y), each of which
     may be x or f."""
-    import torch
+    torch = _t()
     h, y = (None, None) if out is None else out
     shape = _norm_shape(x, f, gate, w_post, w_pre, mod_scale, mod_shift, norm, eps, alpha, h=h, y=y)
     device = _on_gpu(x)
@@ -683,7 +695,7 @@ def gate_residual_norm_backward(x, f, dy, dh, gate=None, w_post=None, w_pre=None
                                 alpha: float = 1.0, stream=None):
     """dx, df, dgate, dw_post, dw_pre, dmod_scale, dmod_shift of gate_residual_norm: None for what
     was not given (dmod_shift with mod_shift). f, and one of dy and dh, may be None."""
-    import torch
+    torch = _t()
     shape = _norm_shape(x, f, gate, w_post, w_pre, mod_scale, mod_shift, norm, eps, alpha, dy=dy, dh=dh)
     device = _on_gpu(x)
     grads = [None if t is None else torch.empty_like(t)

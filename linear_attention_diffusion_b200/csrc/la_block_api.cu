@@ -47,7 +47,7 @@ la_status check_workspace(const void* ws, size_t ws_bytes, size_t need) {
   return LA_OK;
 }
 
-la_status make_gated(const la_gated_shape* s, GatedProblem& p) {
+la_status make_gated(const la_gated_shape* s, bool backward, GatedProblem& p) {
   if (s == nullptr) return fail(LA_ERR_INVALID_ARG, "shape is NULL");
   if (s->B < 0 || s->N < 0 || s->H < 0)
     return fail(LA_ERR_INVALID_ARG, "negative size B=%d N=%d H=%d", s->B, s->N, s->H);
@@ -64,7 +64,7 @@ la_status make_gated(const la_gated_shape* s, GatedProblem& p) {
   p.H = s->H;
   p.io = s->io_dtype;
   p.scale = s->scale;
-  gated_split(p);
+  gated_split(p, backward);
   return LA_OK;
 }
 
@@ -109,7 +109,7 @@ extern "C" {
 
 size_t la_gated_workspace_bytes(const la_gated_shape* shape, int backward) {
   GatedProblem p;
-  if (make_gated(shape, p) != LA_OK) return 0;
+  if (make_gated(shape, backward != 0, p) != LA_OK) return 0;
   const size_t n = gated_need(p, backward != 0);
   return n == 0 ? 256 : n;
 }
@@ -118,7 +118,7 @@ la_status la_gated_attention(const la_gated_shape* shape, const void* Q, const v
                              const void* V, const float* G, const float* S_in, float* S_out,
                              void* O, void* ws, size_t ws_bytes, la_stream stream) {
   GatedProblem p;
-  LA_TRY(make_gated(shape, p));
+  LA_TRY(make_gated(shape, false, p));
   const bool any_state = p.B > 0 && p.H > 0, any = any_state && p.N > 0;
   LA_TRY(check_ptr(Q, "Q", any));
   LA_TRY(check_ptr(K, "K", any));
@@ -153,7 +153,7 @@ la_status la_gated_attention_backward(const la_gated_shape* shape, const void* Q
                                       void* dV, float* dG, float* dS_in, void* ws,
                                       size_t ws_bytes, la_stream stream) {
   GatedProblem p;
-  LA_TRY(make_gated(shape, p));
+  LA_TRY(make_gated(shape, true, p));
   const bool any_state = p.B > 0 && p.H > 0, any = any_state && p.N > 0;
   LA_TRY(check_ptr(Q, "Q", any));
   LA_TRY(check_ptr(K, "K", any));

@@ -22,7 +22,7 @@ constexpr int kGateBlock = 16;      // tokens of one tensor-core block
 constexpr int kGateStepTokens = 8;  // up to here tokens are walked one by one
 constexpr int kGateAnchor = 256;    // tokens between two stored states of the backward
 
-void gated_split(GatedProblem& p);
+void gated_split(GatedProblem& p, bool backward);
 size_t gated_workspace_floats(const GatedProblem& p, bool backward);
 cudaError_t launch_gated(const GatedProblem& p, const void* Q, const void* K, const void* V,
                          const float* G, const float* S_in, float* S_out, void* O, float* ws,

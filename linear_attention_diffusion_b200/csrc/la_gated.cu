@@ -28,12 +28,16 @@
 // products, and set afresh to <U, S> every kGateAnchor tokens, where the first walk
 // has left its S: rounding errors of the sum do not grow with the length.
 #include "la_gated.cuh"
+#include "la_sm100.cuh"
 
 namespace la {
 namespace gated {
 namespace {
 
-constexpr int kWarps = 4;  // warps of a CTA: neighbouring heads of one segment
+// Warps of a CTA: neighbouring heads of one segment. Float32 warps need 22 to 29 KB of shared
+// memory each; pairs of them pack the SM better than fours.
+template <int NP>
+constexpr int kWarps = NP == 1 ? 4 : 2;
 
 template <bool k>
 struct Const {
@@ -131,7 +135,8 @@ __device__ __forceinline__ void block_row(float (&acc)[4][4], int b, const Frag<
 // kExact: the state's own update keeps 24 bits, for a state that goes out in float32 or stands
 // behind a float32 gradient; else 17, as many as a bf16 output can show.
 template <int NP, bool kBack, bool kExact, int kStages>
-__global__ void __launch_bounds__(kWarps * 32, 3) walk_kernel(const Walk a) {
+__global__ void __launch_bounds__(kWarps<NP> * 32, kBack ? (NP == 1 ? 2 : 4) : NP == 1 ? 3 : 5)
+walk_kernel(const Walk a) {
   using T = typename Io<NP>::T;
   constexpr int NB = kBlocks<NP>, NT = kBack ? 4 : 3, NC = parts(NP, kBack);
   constexpr int kStep = NB * kGateBlock;
@@ -139,7 +144,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) walk_kernel(const Walk a) {
   extern __shared__ __align__(128) uint8_t smem_all[];
   const GatedProblem& p = a.p;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long unit = static_cast<long long>(blockIdx.x) * kWarps + warp;
+  const long long unit = static_cast<long long>(blockIdx.x) * kWarps<NP> + warp;
   if (unit >= static_cast<long long>(p.B) * p.H * p.nseg) return;
   const Place<NB> at(p, unit);
   const T* heads[NT];
@@ -154,6 +159,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) walk_kernel(const Walk a) {
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) ring.issue(lane);
   Out<NP> out(a.o, at.base, p.H, at.n_begin, lane);
+  sm100::pdl_trigger();
+  sm100::pdl_wait();  // the inputs were there before; the states come from the kernel before
 
   State S;
   if (p.nseg > 1)
@@ -272,7 +279,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) walk_kernel(const Walk a) {
 // forward, w = dO. The carried state X (rows: k's dimensions, columns: v's) is the
 // gradient that reaches the state at a step's end from later tokens.
 template <int NP, int kStages>
-__global__ void __launch_bounds__(kWarps * 32, NP == 3 ? 2 : 3) walk_back_kernel(const Walk a) {
+__global__ void __launch_bounds__(kWarps<NP> * 32, NP == 1 ? 2 : 3)
+walk_back_kernel(const Walk a) {
   using T = typename Io<NP>::T;
   constexpr int NB = kBlocks<NP>, NT = 4, NK = parts(NP, true), NV = parts(NP, false);
   constexpr int kStep = NB * kGateBlock;
@@ -280,13 +288,14 @@ __global__ void __launch_bounds__(kWarps * 32, NP == 3 ? 2 : 3) walk_back_kernel
   extern __shared__ __align__(128) uint8_t smem_all[];
   const GatedProblem& p = a.p;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long unit = static_cast<long long>(blockIdx.x) * kWarps + warp;
+  const long long unit = static_cast<long long>(blockIdx.x) * kWarps<NP> + warp;
   if (unit >= static_cast<long long>(p.B) * p.H * p.nseg) return;
   const Place<NB> at(p, unit);
   const T* const heads[NT] = {static_cast<const T*>(a.k) + at.base, static_cast<const T*>(a.v) + at.base,
                               static_cast<const T*>(a.q) + at.base, static_cast<const T*>(a.w) + at.base};
   const uint32_t smem = smem_addr(smem_all) + warp * M::kWarp;
   const uint32_t planes = smem + kStages * M::kStage;
+  sm100::pdl_wait();  // rows, anchors and states come from the kernels before
   int n0 = at.n_begin + (at.iters - 1) * kStep;  // the last step comes first
   Ring<NP, NB, NT, kStages, NT, true, true> ring(smem, heads, a.G + at.gbase, p.H,
                                                  a.rows + static_cast<size_t>(at.bh) * p.N, n0,
@@ -448,7 +457,7 @@ __global__ void __launch_bounds__(kWarps * 32, NP == 3 ? 2 : 3) walk_back_kernel
 // segments' first tokens, the walk reads first, while it is still in L2. Once the decay to
 // the segment's end has become 0, no earlier token has a part in S.
 template <int NP, bool kBack, int kStages>
-__global__ void __launch_bounds__(kWarps * 32, NP == 1 && !kBack ? 4 : 3)
+__global__ void __launch_bounds__(kWarps<NP> * 32, kBack ? (NP == 1 ? 3 : 4) : NP == 1 ? 4 : 5)
 segment_kernel(const GatedProblem p, int segs, const void* qv, const void* kv, const void* vv,
                const void* dov, const float* Gv, float* states, float* last_states, float* grads,
                float* decays) {
@@ -458,7 +467,7 @@ segment_kernel(const GatedProblem p, int segs, const void* qv, const void* kv, c
   using M = Smem<NP, NB, NT, kStages>;
   extern __shared__ __align__(128) uint8_t smem_all[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long unit = static_cast<long long>(blockIdx.x) * kWarps + warp;
+  const long long unit = static_cast<long long>(blockIdx.x) * kWarps<NP> + warp;
   if (unit >= static_cast<long long>(p.B) * p.H * segs) return;
   const Place<NB> at(p, unit);
   const T* heads[NT];
@@ -468,6 +477,7 @@ segment_kernel(const GatedProblem p, int segs, const void* qv, const void* kv, c
     heads[NT - 2] = static_cast<const T*>(qv) + at.base;
     heads[NT - 1] = static_cast<const T*>(dov) + at.base;
   }
+  sm100::pdl_trigger();
   const uint32_t smem = smem_addr(smem_all) + warp * M::kWarp;
   const uint32_t planes = smem + kStages * M::kStage;
   Ring<NP, NB, NT, kStages, NT, true, false> ring(smem, heads, Gv + at.gbase, p.H, nullptr,
@@ -556,6 +566,8 @@ combine_kernel(int nseg, const float* decays, float* states, const float* s_init
                const float* x_init, const float* tail_state, float* s_final) {
   const int bh = blockIdx.x, f = blockIdx.y * 64 + threadIdx.x;
   const bool back = blockIdx.z == 1;
+  sm100::pdl_trigger();
+  sm100::pdl_wait();
   float4* slot = reinterpret_cast<float4*>(back ? grads : states) +
                  static_cast<size_t>(bh) * nseg * 256 + f;
   const float* init = back ? x_init : s_init;
@@ -643,7 +655,7 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&x)[4]) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(128, 8)
 step_kernel(const GatedProblem p, const T* Q, const T* K, const T* V, const float* G,
             const float* S_in, float* S_out, T* O) {
   const int lane = threadIdx.x & 31;
@@ -693,12 +705,33 @@ step_kernel(const GatedProblem p, const T* Q, const T* K, const T* V, const floa
   }
 }
 
-template <typename Kernel>
-cudaError_t allow_smem(Kernel k, int bytes) {
-  return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+// Launch a kernel with its shared memory. chained: it may start while the kernel before it on
+// the stream, one of this call's own, still runs, and waits for it itself (pdl_wait).
+template <typename... Params, typename... Args>
+cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, int smem, bool chained,
+                   cudaStream_t s, Args... args) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = chained ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
 }
 
-unsigned grid_of(long long units) { return static_cast<unsigned>((units + kWarps - 1) / kWarps); }
+template <int NP>
+dim3 grid_of(long long units) {
+  return dim3(static_cast<unsigned>((units + kWarps<NP> - 1) / kWarps<NP>));
+}
 
 template <int NP>
 cudaError_t forward(const GatedProblem& p, const void* Q, const void* K, const void* V,
@@ -711,16 +744,14 @@ cudaError_t forward(const GatedProblem& p, const void* Q, const void* K, const v
   float* decays = last_states + BH * 1024;
   cudaError_t e;
   if (p.nseg > 1) {
-    auto seg = segment_kernel<NP, false, kSegStages>;
-    const int bytes = kWarps * Smem<NP, NB, 2, kSegStages>::kWarp;
-    if ((e = allow_smem(seg, bytes)) != cudaSuccess) return e;
     const int segs = S_out != nullptr ? p.nseg : p.nseg - 1;
-    seg<<<grid_of(BH * segs), kWarps * 32, bytes, s>>>(p, segs, Q, K, V, nullptr, G, states,
-                                                       last_states, nullptr, decays);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    combine_kernel<true><<<dim3(static_cast<unsigned>(BH), 4, 1), 64, 0, s>>>(
-        p.nseg, decays, states, S_in, nullptr, nullptr, last_states, S_out);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch(segment_kernel<NP, false, kSegStages>, grid_of<NP>(BH * segs), kWarps<NP> * 32,
+               kWarps<NP> * Smem<NP, NB, 2, kSegStages>::kWarp, false, s, p, segs, Q, K, V, nullptr,
+               G, states, last_states, nullptr, decays);
+    if (e != cudaSuccess) return e;
+    e = launch(combine_kernel<true>, dim3(static_cast<unsigned>(BH), 4, 1), 64, 0, true, s, p.nseg,
+               decays, states, S_in, nullptr, nullptr, last_states, S_out);
+    if (e != cudaSuccess) return e;
   }
   Walk a = {};
   a.q = Q;
@@ -736,10 +767,8 @@ cudaError_t forward(const GatedProblem& p, const void* Q, const void* K, const v
   if constexpr (NP == 1) {
     if (a.final_ == nullptr) walk = walk_kernel<NP, false, false, kStages>;
   }
-  const int bytes = kWarps * Smem<NP, NB, 3, kStages, 3>::kWarp;
-  if ((e = allow_smem(walk, bytes)) != cudaSuccess) return e;
-  walk<<<grid_of(BH * p.nseg), kWarps * 32, bytes, s>>>(a);
-  return cudaGetLastError();
+  return launch(walk, grid_of<NP>(BH * p.nseg), kWarps<NP> * 32,
+                kWarps<NP> * Smem<NP, NB, 3, kStages, 3>::kWarp, p.nseg > 1, s, a);
 }
 
 // Anchors of a segment: at its start and every kGateAnchor tokens after it.
@@ -750,7 +779,7 @@ cudaError_t backward(const GatedProblem& p, const void* Q, const void* K, const 
                      const float* G, const float* S_in, const void* dO, const float* dS_out,
                      void* dQ, void* dK, void* dV, float* dG, float* dS_in, float* ws,
                      cudaStream_t s) {
-  constexpr int NB = kBlocks<NP>, kStages = 2;
+  constexpr int NB = kBlocks<NP>, kStages = NP == 1 ? 3 : 2;
   const long long BH = 1LL * p.B * p.H;
   Walk a = {};
   a.anchor = kGateAnchor;
@@ -760,17 +789,17 @@ cudaError_t backward(const GatedProblem& p, const void* Q, const void* K, const 
   a.anchors = grads + BH * p.nseg * 1024;
   a.rows = a.anchors + BH * (1LL * p.nseg * a.per_seg + 1) * 1024;
   float* decays = a.rows + (BH * p.N + 3) / 4 * 4;
+  const int threads = kWarps<NP> * 32, smem = kWarps<NP> * Smem<NP, NB, 4, kStages>::kWarp;
+  const dim3 grid = grid_of<NP>(BH * p.nseg);
   cudaError_t e;
   if (p.nseg > 1) {
-    auto seg = segment_kernel<NP, true, kStages>;
-    const int bytes = kWarps * Smem<NP, NB, 4, kStages>::kWarp;
-    if ((e = allow_smem(seg, bytes)) != cudaSuccess) return e;
-    seg<<<grid_of(BH * p.nseg), kWarps * 32, bytes, s>>>(p, p.nseg, Q, K, V, dO, G, states, nullptr,
-                                                         grads, decays);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    combine_kernel<false><<<dim3(static_cast<unsigned>(BH), 4, 2), 64, 0, s>>>(
-        p.nseg, decays, states, S_in, grads, dS_out, nullptr, nullptr);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch(segment_kernel<NP, true, 2>, grid, threads,
+               kWarps<NP> * Smem<NP, NB, 4, 2>::kWarp, false, s, p, p.nseg, Q, K, V, dO, G, states,
+               nullptr, grads, decays);
+    if (e != cudaSuccess) return e;
+    e = launch(combine_kernel<false>, dim3(static_cast<unsigned>(BH), 4, 2), 64, 0, true, s, p.nseg,
+               decays, states, S_in, grads, dS_out, nullptr, nullptr);
+    if (e != cudaSuccess) return e;
   }
   a.G = G;
   a.p = p;
@@ -781,11 +810,9 @@ cudaError_t backward(const GatedProblem& p, const void* Q, const void* K, const 
   a.o = dQ;
   a.init = S_in;
   a.prefix = states;
-  auto walk = walk_kernel<NP, true, true, kStages>;
-  int bytes = kWarps * Smem<NP, NB, 4, kStages, 3>::kWarp;
-  if ((e = allow_smem(walk, bytes)) != cudaSuccess) return e;
-  walk<<<grid_of(BH * p.nseg), kWarps * 32, bytes, s>>>(a);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch(walk_kernel<NP, true, true, kStages>, grid, threads,
+             kWarps<NP> * Smem<NP, NB, 4, kStages, 3>::kWarp, p.nseg > 1, s, a);
+  if (e != cudaSuccess) return e;
   a.q = Q;
   a.k = K;
   a.v = V;
@@ -796,21 +823,19 @@ cudaError_t backward(const GatedProblem& p, const void* Q, const void* K, const 
   a.final_ = dS_in;
   a.prefix = grads;
   a.dG = dG;
-  auto back = walk_back_kernel<NP, kStages>;
-  bytes = kWarps * Smem<NP, NB, 4, kStages>::kWarp;
-  if ((e = allow_smem(back, bytes)) != cudaSuccess) return e;
-  back<<<grid_of(BH * p.nseg), kWarps * 32, bytes, s>>>(a);
-  return cudaGetLastError();
+  return launch(walk_back_kernel<NP, kStages>, grid, threads, smem, true, s, a);
 }
 
 }  // namespace
 }  // namespace gated
 
-// Segments: as many as fill one wave of warps (12 on each of 148 SMs), none below 64
-// tokens, where a warp's start and the extra states would cost more than they give.
-void gated_split(GatedProblem& p) {
+// Segments: as many as fill one wave of warps on 148 SMs, none below 64 tokens, where a warp's
+// start and the extra states would cost more than they give. Warps that fit on an SM: by
+// registers (bf16: 168 a thread forwards, 255 backwards) or shared memory (float32).
+void gated_split(GatedProblem& p, bool backward) {
   const long long BH = 1LL * p.B * p.H;
-  long long n = BH > 0 ? 148LL * 12 / BH : 1;
+  const long long per_sm = p.io == LA_IO_BF16 ? (backward ? 8 : 12) : (backward ? 6 : 10);
+  long long n = BH > 0 ? 148LL * per_sm / BH : 1;
   if (n < 1) n = 1;
   long long seg = (p.N + n - 1) / n;
   if (seg < 64) seg = 64;

@@ -14,12 +14,13 @@
 // w_pre (1 + scale); shift): read per row from global memory they would be more bytes
 // than the row. So a CTA keeps to one batch element.
 //
-// Backward: a thread owns 8 columns (16 in rows over 2560) of all its CTA's rows and sums the three
+// Backward: a thread owns 16 columns of all its CTA's rows and sums the three
 // column sums that the parameters' gradients need, sum dy n, sum dy and sum u dh, in
 // registers; a second kernel adds the CTAs' partial sums in order. No atomics: the
 // same bits every time.
 #include "la_block_internal.h"
 #include "la_common.cuh"
+#include "la_sm100.cuh"
 
 namespace la {
 namespace {
@@ -43,6 +44,7 @@ struct Raw<__nv_bfloat16> {
     }
   }
   __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+
 };
 template <>
 struct Raw<float> {
@@ -56,6 +58,7 @@ struct Raw<float> {
     x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+
 };
 
 // A vector of C floats in shared memory: the first four of every eight columns, then the
@@ -74,29 +77,50 @@ struct Line {
   }
 };
 
-// Sums over the threads of a row: a warp's shuffles, then (kOneWarp = false) one word per
-// warp. `slot` alternates between two sets, so one barrier per sum is enough.
-template <bool kOneWarp, int kN>
-__device__ __forceinline__ void row_sum(float (&x)[kN], float* scratch, int& slot) {
+// Sums over the threads of a row: a warp's shuffles, then (kWarps > 1) one word per warp in
+// shared memory, read back as whole lines (words of warps that a CTA lacks stay 0). `slot`
+// alternates between two sets, so one barrier per sum is enough. Two sums go through the
+// shuffles together: after the first step one half of the warp carries each.
+constexpr int kScratch = 2 * 2 * 32;  // floats: slots x sums x warps
+
+template <int kWarps>
+__device__ __forceinline__ float across_warps(const float* s) {
+  float t = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kN; ++i)
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) x[i] += __shfl_xor_sync(0xffffffffu, x[i], d);
-  if (kOneWarp) return;
-  float* s = scratch + slot * 64;
-  slot ^= 1;
-  const int warps = blockDim.x >> 5;
-  if ((threadIdx.x & 31) == 0) {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) s[i * 32 + (threadIdx.x >> 5)] = x[i];
+  for (int i = 0; i < (kWarps + 3) / 4; ++i) {
+    const float4 v = reinterpret_cast<const float4*>(s)[i];
+    t += (v.x + v.y) + (v.z + v.w);
   }
+  return t;
+}
+template <int kWarps>
+__device__ __forceinline__ float row_sum(float x, float* scratch, int& slot) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+  if (kWarps == 1) return x;
+  float* s = scratch + slot;
+  slot ^= 64;
+  if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
   __syncthreads();
+  return across_warps<kWarps>(s);
+}
+template <int kWarps>
+__device__ __forceinline__ void row_sum2(float& x, float& y, float* scratch, int& slot) {
+  const bool low = (threadIdx.x & 16) == 0;
+  float z = __shfl_xor_sync(0xffffffffu, low ? y : x, 16) + (low ? x : y);
 #pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    float t = 0.0f;
-    for (int w = 0; w < warps; ++w) t += s[i * 32 + w];
-    x[i] = t;
+  for (int d = 8; d > 0; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+  if (kWarps == 1) {
+    x = __shfl_sync(0xffffffffu, z, 0);
+    y = __shfl_sync(0xffffffffu, z, 16);
+    return;
   }
+  float* s = scratch + slot;
+  slot ^= 64;
+  if ((threadIdx.x & 15) == 0) s[(low ? 0 : 32) + (threadIdx.x >> 5)] = z;
+  __syncthreads();
+  x = across_warps<kWarps>(s);
+  y = across_warps<kWarps>(s + 32);
 }
 
 // Per-channel factors of batch element b: alpha gate w_post, w_pre (1 + scale), shift.
@@ -124,6 +148,8 @@ norm_kernel(const NormProblem p, const T* x, const T* f, const NormParams w, T* 
   const int vecs = p.C / kVec, b = blockIdx.y;
   const Line l1 = {smem, vecs}, l2 = {smem + p.C, vecs}, l3 = {smem + 2 * p.C, vecs};
   float* scratch = smem + 3 * p.C;
+  constexpr int kRowWarps = kOneWarp ? 1 : 32;
+  for (int i = threadIdx.x; i < kScratch; i += blockDim.x) scratch[i] = 0.0f;
   combine_params(p, w, b, l1, l2, &l3);
   __syncthreads();
   const int width = kOneWarp ? 32 : blockDim.x;  // threads of a row
@@ -147,16 +173,15 @@ norm_kernel(const NormProblem p, const T* x, const T* f, const NormParams w, T* 
     }
     float rstd_f = 1.0f;
     if (w.w_post != nullptr) {
-      float s[1] = {0.0f};
+      float s = 0.0f;
 #pragma unroll
       for (int k = 0; k < KV; ++k) {
         float a[8];
         rf[k].get(a);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[0] = fmaf(a[i], a[i], s[0]);
+        for (int i = 0; i < 8; ++i) s = fmaf(a[i], a[i], s);
       }
-      row_sum<kOneWarp>(s, scratch, slot);
-      rstd_f = rsqrtf(fmaf(s[0], inv, p.eps));
+      rstd_f = rsqrtf(fmaf(row_sum<kRowWarps>(s, scratch, slot), inv, p.eps));
     }
     float r[KV][8];
 #pragma unroll
@@ -175,26 +200,24 @@ norm_kernel(const NormProblem p, const T* x, const T* f, const NormParams w, T* 
     if (y == nullptr) continue;
     float mean = 0.0f;
     if (p.layer) {
-      float s[1] = {0.0f};
+      float s = 0.0f;
 #pragma unroll
       for (int k = 0; k < KV; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[0] += r[k][i];
-      row_sum<kOneWarp>(s, scratch, slot);
-      mean = s[0] * inv;
+        for (int i = 0; i < 8; ++i) s += r[k][i];
+      mean = row_sum<kRowWarps>(s, scratch, slot) * inv;
     }
-    float s[1] = {0.0f};
+    float s = 0.0f;
 #pragma unroll
     for (int k = 0; k < KV; ++k)
       if (t + k * width < vecs) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           r[k][i] -= mean;
-          s[0] = fmaf(r[k][i], r[k][i], s[0]);
+          s = fmaf(r[k][i], r[k][i], s);
         }
       }
-    row_sum<kOneWarp>(s, scratch, slot);
-    const float rstd = rsqrtf(fmaf(s[0], inv, p.eps));
+    const float rstd = rsqrtf(fmaf(row_sum<kRowWarps>(s, scratch, slot), inv, p.eps));
 #pragma unroll
     for (int k = 0; k < KV; ++k) {
       const int v = t + k * width;
@@ -210,24 +233,45 @@ norm_kernel(const NormProblem p, const T* x, const T* f, const NormParams w, T* 
   }
 }
 
-// Threads of a backward CTA with one and with two vectors each: the most that leaves a thread
-// the registers for its column sums and the next row.
-constexpr int kOneThreads = 320, kTwoThreads = 512;
-static_assert(kTwoThreads * 2 * kVec == kNormMaxC, "the widest row");
+// A backward thread owns two vectors of every row: the sums over a row cost each thread its
+// shuffles and a barrier, which 16 columns pay for better than 8. The next row is on its way
+// to shared memory meanwhile, every thread its own pieces, so nothing but the thread waits
+// for them; in registers they would spill its column sums.
+constexpr int kBackVecs = 2, kNarrow = 160, kWide = 512;
+static_assert(kWide * kBackVecs * kVec == kNormMaxC, "the widest row");
+
+// Shared memory as a 32-bit address.
+__device__ __forceinline__ float4 lds4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void widen(float4 a, float4 b, float (&x)[8]) {
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
 
 // Backward of one batch element's rows; `part`: [B][CTAs][3][C] column sums (sum dy n, sum dy,
 // sum u dh).
-template <typename T, int KV, bool kOneWarp>
-__global__ void __launch_bounds__(KV == 1 ? kOneThreads : kTwoThreads, KV == 1 ? 2 : 1)
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == kWide ? 1 : 480 / kThreads)
 norm_backward_kernel(const NormProblem p, const T* x, const T* f, const NormParams w, const T* dh,
                      const T* dy, T* dx, T* df, float* part) {
+  constexpr int KV = kBackVecs, kRowWarps = kThreads / 32;
   extern __shared__ __align__(16) float smem[];
   const int vecs = p.C / kVec, b = blockIdx.y, t = threadIdx.x, width = blockDim.x;
   const Line l1 = {smem, vecs}, l2 = {smem + p.C, vecs};
   float* scratch = smem + 2 * p.C;
+  for (int i = t; i < kScratch; i += width) scratch[i] = 0.0f;
   combine_params(p, w, b, l1, l2, nullptr);
+  sm100::pdl_trigger();
   __syncthreads();
   const float inv = 1.0f / static_cast<float>(p.C);
+  const bool has_f = f != nullptr, has_h = dh != nullptr, has_y = dy != nullptr;
+  const bool post = w.w_post != nullptr;
   int slot = 0;
   float sum_e[KV][8], sum_d[KV][8], sum_f[KV][8];
 #pragma unroll
@@ -235,106 +279,139 @@ norm_backward_kernel(const NormProblem p, const T* x, const T* f, const NormPara
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum_e[k][i] = sum_d[k][i] = sum_f[k][i] = 0.0f;
 
-  Raw<T> rx[KV], rf[KV], rh[KV], ry[KV];
-  auto load = [&](int n) {
-    const size_t row = (static_cast<size_t>(b) * p.N + n) * p.C;
+  // The thread's vectors t and t + width; the second may be missing. Byte offsets in a row, in
+  // the factors, and in the pieces of the next row: [tensor][vector][16 bytes][thread].
+  constexpr int kPieces = kVec * sizeof(T) / 16;
+  const bool have[KV] = {t < vecs, t + width < vecs};
+  const uint32_t base = sm100::smem_u32(smem);
+  const uint32_t m1 = base + t * 16, m2 = m1 + p.C * 4, upper = vecs * 16, next = width * 16;
+  const uint32_t ahead = base + (2 * p.C + kScratch) * 4 + t * 16;
+  const size_t pitch = static_cast<size_t>(p.C) * sizeof(T);
+  const size_t move = pitch * gridDim.x;
+  size_t ofs = (static_cast<size_t>(b) * p.N + blockIdx.x) * pitch + t * kVec * sizeof(T);
+  const uint32_t second = width * kVec * sizeof(T);
+  auto fetch = [&](int n, size_t at) {
+    if (n < p.N) {
+      auto tensor = [&](int a, const T* src) {
+        const char* q = reinterpret_cast<const char*>(src) + at;
 #pragma unroll
-    for (int k = 0; k < KV; ++k) {
-      const int v = t + k * width;
-      rx[k].zero();
-      rf[k].zero();
-      rh[k].zero();
-      ry[k].zero();
-      if (n < p.N && v < vecs) {
-        rx[k].load(x + row + v * kVec);
-        if (f != nullptr) rf[k].load(f + row + v * kVec);
-        if (dh != nullptr) rh[k].load(dh + row + v * kVec);
-        if (dy != nullptr) ry[k].load(dy + row + v * kVec);
+        for (int k = 0; k < KV; ++k)
+          if (have[k]) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                               ahead + ((a * KV + k) * kPieces + i) * next),
+                           "l"(q + k * second + i * 16)
+                           : "memory");
+          }
+      };
+      tensor(0, x);
+      if (has_f) tensor(1, f);
+      if (has_h) tensor(2, dh);
+      if (has_y) tensor(3, dy);
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto take = [&](int a, int k, bool there, float (&out)[8]) {
+    if (there && have[k]) {
+      const uint32_t at = ahead + (a * KV + k) * kPieces * next;
+      const float4 v = lds4(at);
+      if (sizeof(T) == 2) {
+        Raw<__nv_bfloat16> r;
+        r.u = make_uint4(__float_as_uint(v.x), __float_as_uint(v.y), __float_as_uint(v.z),
+                         __float_as_uint(v.w));
+        r.get(out);
+      } else {
+        widen(v, lds4(at + next), out);
       }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) out[i] = 0.0f;
     }
   };
-  constexpr bool kAhead = KV == 1;  // registers for the next row too
-  if (kAhead) load(blockIdx.x);
-  for (int n = blockIdx.x; n < p.N; n += gridDim.x) {
-    const size_t row = (static_cast<size_t>(b) * p.N + n) * p.C;
-    if (!kAhead) load(n);
+  auto factors = [&](uint32_t line, int k, float (&m)[8]) {
+    widen(lds4(line + k * next), lds4(line + upper + k * next), m);
+  };
+  fetch(blockIdx.x, ofs);
+  for (int n = blockIdx.x; n < p.N; n += gridDim.x, ofs += move) {
     float hx[KV][8], u[KV][8], g[KV][8], gy[KV][8];  // h, u / w_post, dh, dy
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
     for (int k = 0; k < KV; ++k) {
-      rx[k].get(hx[k]);
-      rf[k].get(u[k]);
-      rh[k].get(g[k]);
-      ry[k].get(gy[k]);
+      take(0, k, true, hx[k]);
+      take(1, k, has_f, u[k]);
+      take(2, k, has_h, g[k]);
+      take(3, k, has_y, gy[k]);
     }
-    if (kAhead) load(n + gridDim.x);  // the next row is on its way while this one is worked on
+    fetch(n + gridDim.x, ofs + move);
     float rstd_f = 1.0f;
-    if (w.w_post != nullptr) {
-      float s[1] = {0.0f};
+    if (post) {
+      float s = 0.0f;
 #pragma unroll
       for (int k = 0; k < KV; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[0] = fmaf(u[k][i], u[k][i], s[0]);
-      row_sum<kOneWarp>(s, scratch, slot);
-      rstd_f = rsqrtf(fmaf(s[0], inv, p.eps));
-    }
-    if (f != nullptr) {
+        for (int i = 0; i < 8; ++i) s = fmaf(u[k][i], u[k][i], s);
+      rstd_f = rsqrtf(fmaf(row_sum<kRowWarps>(s, scratch, slot), inv, p.eps));
 #pragma unroll
-      for (int k = 0; k < KV; ++k) {
-        const int v = t + k * width;
-        if (v < vecs) {
+      for (int k = 0; k < KV; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) u[k][i] *= rstd_f;
+    }
+    if (has_f) {
+#pragma unroll
+      for (int k = 0; k < KV; ++k)
+        if (have[k]) {
           float m[8];
-          l1.get(v, m);
+          factors(m1, k, m);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            u[k][i] *= rstd_f;
-            hx[k][i] = fmaf(u[k][i], m[i], hx[k][i]);
-          }
+          for (int i = 0; i < 8; ++i) hx[k][i] = fmaf(u[k][i], m[i], hx[k][i]);
         }
-      }
     }
-    if (dy != nullptr) {
+    if (has_y) {
       float mean = 0.0f;
       if (p.layer) {
-        float s[1] = {0.0f};
+        float s = 0.0f;
 #pragma unroll
         for (int k = 0; k < KV; ++k)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) s[0] += hx[k][i];
-        row_sum<kOneWarp>(s, scratch, slot);
-        mean = s[0] * inv;
+          for (int i = 0; i < 8; ++i) s += hx[k][i];
+        mean = row_sum<kRowWarps>(s, scratch, slot) * inv;
       }
-      float s[1] = {0.0f};
+      float s = 0.0f;
 #pragma unroll
       for (int k = 0; k < KV; ++k)
-        if (t + k * width < vecs) {
+        if (have[k]) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             hx[k][i] -= mean;
-            s[0] = fmaf(hx[k][i], hx[k][i], s[0]);
+            s = fmaf(hx[k][i], hx[k][i], s);
           }
         }
-      row_sum<kOneWarp>(s, scratch, slot);
-      const float rstd = rsqrtf(fmaf(s[0], inv, p.eps));
-      float s2[2] = {0.0f, 0.0f};
+      const float rstd = rsqrtf(fmaf(row_sum<kRowWarps>(s, scratch, slot), inv, p.eps));
+      float along = 0.0f, off = 0.0f;  // the parts of t = dy w_pre (1 + scale) along n and 1
 #pragma unroll
-      for (int k = 0; k < KV; ++k) {
-        const int v = t + k * width;
-        if (v < vecs) {
+      for (int k = 0; k < KV; ++k)
+        if (have[k]) {
           float m[8];
-          l2.get(v, m);
+          factors(m2, k, m);
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             hx[k][i] *= rstd;  // n
             sum_e[k][i] = fmaf(gy[k][i], hx[k][i], sum_e[k][i]);
             sum_d[k][i] += gy[k][i];
             gy[k][i] *= m[i];
-            s2[0] = fmaf(gy[k][i], hx[k][i], s2[0]);
-            s2[1] += gy[k][i];
+            along = fmaf(gy[k][i], hx[k][i], along);
+            off += gy[k][i];
           }
         }
+      if (p.layer) {
+        row_sum2<kRowWarps>(along, off, scratch, slot);
+      } else {
+        along = row_sum<kRowWarps>(along, scratch, slot);
+        off = 0.0f;
       }
-      row_sum<kOneWarp>(s2, scratch, slot);
-      const float along = s2[0] * inv, off = p.layer ? s2[1] * inv : 0.0f;
+      along *= inv;
+      off *= inv;
 #pragma unroll
       for (int k = 0; k < KV; ++k)
 #pragma unroll
@@ -342,45 +419,40 @@ norm_backward_kernel(const NormProblem p, const T* x, const T* f, const NormPara
           g[k][i] = fmaf(rstd, gy[k][i] - fmaf(hx[k][i], along, off), g[k][i]);
     }
 #pragma unroll
-    for (int k = 0; k < KV; ++k) {
-      const int v = t + k * width;
-      if (v < vecs) store_row<8>(dx + row + v * kVec, g[k]);
-    }
-    if (f == nullptr) continue;
-    float s[1] = {0.0f};
+    for (int k = 0; k < KV; ++k)
+      if (have[k])
+        store_row<8>(reinterpret_cast<T*>(reinterpret_cast<char*>(dx) + ofs + k * second), g[k]);
+    if (!has_f) continue;
+    float s = 0.0f;
 #pragma unroll
-    for (int k = 0; k < KV; ++k) {
-      const int v = t + k * width;
-      if (v < vecs) {
+    for (int k = 0; k < KV; ++k)
+      if (have[k]) {
         float m[8];
-        l1.get(v, m);
+        factors(m1, k, m);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           sum_f[k][i] = fmaf(u[k][i], g[k][i], sum_f[k][i]);
           g[k][i] *= m[i];
-          s[0] = fmaf(g[k][i], u[k][i], s[0]);
+          s = fmaf(g[k][i], u[k][i], s);
         }
       }
-    }
-    if (w.w_post != nullptr) {
-      row_sum<kOneWarp>(s, scratch, slot);
-      const float along = s[0] * inv;
+    if (post) {
+      const float part_u = row_sum<kRowWarps>(s, scratch, slot) * inv;
 #pragma unroll
       for (int k = 0; k < KV; ++k)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[k][i] = rstd_f * (g[k][i] - u[k][i] * along);
+        for (int i = 0; i < 8; ++i) g[k][i] = rstd_f * (g[k][i] - u[k][i] * part_u);
     }
 #pragma unroll
-    for (int k = 0; k < KV; ++k) {
-      const int v = t + k * width;
-      if (v < vecs) store_row<8>(df + row + v * kVec, g[k]);
-    }
+    for (int k = 0; k < KV; ++k)
+      if (have[k])
+        store_row<8>(reinterpret_cast<T*>(reinterpret_cast<char*>(df) + ofs + k * second), g[k]);
   }
   float* out = part + (static_cast<size_t>(b) * gridDim.x + blockIdx.x) * 3 * p.C;
 #pragma unroll
   for (int k = 0; k < KV; ++k) {
     const int v = t + k * width;
-    if (v < vecs) {
+    if (have[k]) {
       store_row<8>(out + v * kVec, sum_e[k]);
       store_row<8>(out + p.C + v * kVec, sum_d[k]);
       store_row<8>(out + 2 * p.C + v * kVec, sum_f[k]);
@@ -389,41 +461,62 @@ norm_backward_kernel(const NormProblem p, const T* x, const T* f, const NormPara
 }
 
 // The parameters' gradients from the CTAs' column sums. blockIdx.y: which of the three sums.
-// 32 columns a CTA; 32 threads per column add the partial sums, always in the same order.
+// 32 columns a CTA; 32 threads per column add the partial sums, always in the same order, of
+// four batch elements at a time (their loads overlap).
 __global__ void __launch_bounds__(1024)
 norm_columns_kernel(const NormProblem p, const NormParams w, const NormGrads g, const float* part) {
-  __shared__ float s[32][33];
+  constexpr int kAtOnce = 4;
+  __shared__ float s[kAtOnce][32][33];
+  sm100::pdl_wait();
   const int which = blockIdx.y;
   float* per_b = which == 0 ? g.mod_scale : which == 1 ? g.mod_shift : g.gate;
   float* over_b = which == 0 ? g.w_pre : which == 1 ? nullptr : g.w_post;
   if (per_b == nullptr && over_b == nullptr) return;
   const int col = threadIdx.x & 31, lane = threadIdx.x >> 5, c = blockIdx.x * 32 + col;
   float total = 0.0f;
-  for (int b = 0; b < p.B; ++b) {
-    float t = 0.0f;
-    if (c < p.C)
-      for (int i = lane; i < p.ctas; i += 32)
-        t += part[((static_cast<size_t>(b) * p.ctas + i) * 3 + which) * p.C + c];
-    s[lane][col] = t;
-    __syncthreads();
-    if (lane == 0 && c < p.C) {
-      t = 0.0f;
+  for (int b0 = 0; b0 < p.B; b0 += kAtOnce) {
+    float t[kAtOnce];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) t += s[i][col];
-      const size_t bc = static_cast<size_t>(b) * p.C + c;
+    for (int k = 0; k < kAtOnce; ++k) t[k] = 0.0f;
+    if (c < p.C) {
+#pragma unroll 2
+      for (int i = lane; i < p.ctas; i += 32)
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k)
+          if (b0 + k < p.B)
+            t[k] += __ldcg(part + ((static_cast<size_t>(b0 + k) * p.ctas + i) * 3 + which) * p.C + c);
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) s[k][lane][col] = t[k];
+    __syncthreads();
+    // warp k adds up batch element b0 + k; thread (k, col) then has its column's sum
+    if (lane < kAtOnce && b0 + lane < p.B && c < p.C) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sum += s[lane][i][col];
+      const size_t bc = static_cast<size_t>(b0 + lane) * p.C + c;
       if (which == 0) {  // sum dy n
-        if (per_b != nullptr) per_b[bc] = t * (w.w_pre != nullptr ? w.w_pre[c] : 1.0f);
-        total = fmaf(t, w.mod_scale != nullptr ? 1.0f + w.mod_scale[bc] : 1.0f, total);
+        if (per_b != nullptr) per_b[bc] = sum * (w.w_pre != nullptr ? w.w_pre[c] : 1.0f);
+        if (w.mod_scale != nullptr) sum *= 1.0f + w.mod_scale[bc];
       } else if (which == 1) {  // sum dy
-        per_b[bc] = t;
+        per_b[bc] = sum;
       } else {  // sum u dh, u without its weight
-        if (per_b != nullptr) per_b[bc] = t * p.alpha * (w.w_post != nullptr ? w.w_post[c] : 1.0f);
-        total = fmaf(t, p.alpha * (w.gate != nullptr ? w.gate[bc] : 1.0f), total);
+        if (per_b != nullptr) per_b[bc] = sum * p.alpha * (w.w_post != nullptr ? w.w_post[c] : 1.0f);
+        sum *= p.alpha * (w.gate != nullptr ? w.gate[bc] : 1.0f);
       }
+      total += sum;
     }
     __syncthreads();
   }
-  if (lane == 0 && c < p.C && over_b != nullptr) over_b[c] = total;
+  if (over_b == nullptr) return;
+  if (lane < kAtOnce) s[0][lane][col] = total;
+  __syncthreads();
+  if (lane == 0 && c < p.C) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) sum += s[0][k][col];
+    over_b[c] = sum;
+  }
 }
 
 template <typename Kernel>
@@ -438,7 +531,7 @@ constexpr long long kSms = 148;
 template <typename T, int KV, bool kOneWarp>
 cudaError_t run_forward(const NormProblem& p, int threads, const void* x, const void* f,
                         const NormParams& w, void* h, void* y, cudaStream_t s) {
-  const size_t smem = (3 * static_cast<size_t>(p.C) + 128) * sizeof(float);
+  const size_t smem = (3 * static_cast<size_t>(p.C) + kScratch) * sizeof(float);
   auto kernel = norm_kernel<T, KV, kOneWarp>;
   cudaError_t e = allow_smem(kernel, smem);
   if (e != cudaSuccess) return e;
@@ -476,17 +569,22 @@ cudaError_t forward(const NormProblem& p, const void* x, const void* f, const No
   return run_forward<T, 1, false>(p, (vecs + 31) / 32 * 32, x, f, w, h, y, s);
 }
 
-template <typename T, int KV, bool kOneWarp>
-cudaError_t run_backward(const NormProblem& p, int threads, const void* x, const void* f,
-                         const NormParams& w, const void* dh, const void* dy, void* dx, void* df,
-                         float* ws, cudaStream_t s) {
-  const size_t smem = (2 * static_cast<size_t>(p.C) + 128) * sizeof(float);
-  auto kernel = norm_backward_kernel<T, KV, kOneWarp>;
+int backward_threads(int C) { return (C + kBackVecs * kVec * 32 - 1) / (kBackVecs * kVec * 32) * 32; }
+
+template <typename T, int kThreads>
+cudaError_t run_backward(const NormProblem& p, const void* x, const void* f, const NormParams& w,
+                         const void* dh, const void* dy, void* dx, void* df, float* ws,
+                         cudaStream_t s) {
+  const int threads = backward_threads(p.C);
+  const size_t smem = (2 * static_cast<size_t>(p.C) + kScratch) * sizeof(float) +
+                      4 * static_cast<size_t>(threads) * kBackVecs * kVec * sizeof(T);
+  auto kernel = norm_backward_kernel<T, kThreads>;
   const cudaError_t e = allow_smem(kernel, smem);
   if (e != cudaSuccess) return e;
   kernel<<<dim3(static_cast<unsigned>(p.ctas), static_cast<unsigned>(p.B)), threads, smem, s>>>(
-      p, static_cast<const T*>(x), static_cast<const T*>(f), w, static_cast<const T*>(dh),
-      static_cast<const T*>(dy), static_cast<T*>(dx), static_cast<T*>(df), ws);
+      p, static_cast<const T*>(x), static_cast<const T*>(f), w,
+                      static_cast<const T*>(dh), static_cast<const T*>(dy), static_cast<T*>(dx),
+                      static_cast<T*>(df), ws);
   return cudaGetLastError();
 }
 
@@ -494,22 +592,19 @@ template <typename T>
 cudaError_t backward(const NormProblem& p, const void* x, const void* f, const NormParams& w,
                      const void* dh, const void* dy, void* dx, void* df, float* ws,
                      cudaStream_t s) {
-  const int vecs = p.C / kVec, one = (vecs + 31) / 32 * 32, two = (vecs + 63) / 64 * 32;
-  if (one == 32) return run_backward<T, 1, true>(p, 32, x, f, w, dh, dy, dx, df, ws, s);
-  if (one <= kOneThreads)
-    return run_backward<T, 1, false>(p, one, x, f, w, dh, dy, dx, df, ws, s);
-  return run_backward<T, 2, false>(p, two, x, f, w, dh, dy, dx, df, ws, s);
+  const int threads = backward_threads(p.C);
+  if (threads == 32) return run_backward<T, 32>(p, x, f, w, dh, dy, dx, df, ws, s);
+  if (threads <= kNarrow) return run_backward<T, kNarrow>(p, x, f, w, dh, dy, dx, df, ws, s);
+  return run_backward<T, kWide>(p, x, f, w, dh, dy, dx, df, ws, s);
 }
 
 }  // namespace
 
-// CTAs of a batch element in the backward: enough warps for the GPU, but at least 8 rows each,
-// so that the partial column sums stay a tenth of the traffic.
+// CTAs of a batch element in the backward: enough warps for the GPU (by registers), but at
+// least 8 rows each, so that the partial column sums stay a tenth of the traffic.
 void norm_split(NormProblem& p) {
-  int threads = (p.C / kVec + 31) / 32 * 32;
-  if (threads > kOneThreads) threads = (p.C / kVec + 63) / 64 * 32;
-  long long per_sm = 640 / (threads > 0 ? threads : 32);
-  per_sm = per_sm < 1 ? 1 : per_sm > 16 ? 16 : per_sm;
+  const int threads = backward_threads(p.C);
+  const long long per_sm = threads <= kNarrow ? 480 / threads : 1;
   long long ctas = p.B > 0 ? (kSms * per_sm + p.B - 1) / p.B : 1;
   const long long most = (p.N + 7) / 8;
   if (ctas > most) ctas = most;
@@ -536,8 +631,16 @@ cudaError_t launch_norm_backward(const NormProblem& p, const void* x, const void
   if (g.gate == nullptr && g.w_post == nullptr && g.w_pre == nullptr && g.mod_scale == nullptr &&
       g.mod_shift == nullptr)
     return cudaSuccess;
-  norm_columns_kernel<<<dim3(static_cast<unsigned>((p.C + 31) / 32), 3), 1024, 0, s>>>(p, w, g, ws);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.C + 31) / 32), 3);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];  // its CTAs may be in place before the sums are done
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_columns_kernel, p, w, g, static_cast<const float*>(ws));
 }
 
 }  // namespace la
