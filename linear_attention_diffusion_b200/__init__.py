@@ -462,13 +462,15 @@ def qkv_state(X, W, bias=None, rope_grid=None, t_offset: int = 0, rope_base: flo
 # stream unless one is given) and take their workspace from torch's allocator.
 
 _torch = None
+_raw_stream = None  # address of a device's current stream without making a Stream object
 
 
 def _t():
     """torch, imported at the first call that needs it."""
-    global _torch
+    global _torch, _raw_stream
     if _torch is None:
         import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         _torch = torch
     return _torch
 
@@ -485,9 +487,8 @@ def _io_of(x, name: str) -> int:
 def _need(name: str, x, shape, dtype, device: int) -> None:
     """Raise ValueError unless x (None is left to the caller) is a contiguous tensor of this
     shape and type on GPU ``device`` (-1: the CPU)."""
-    if x is None:
-        return
-    if x.dtype is not dtype or x.get_device() != device or x.shape != shape or not x.is_contiguous():
+    if x is not None and (x.dtype is not dtype or x.get_device() != device or x.shape != shape
+                          or not x.is_contiguous()):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)} on GPU {device}, got "
                          f"{x.dtype} {tuple(x.shape)} with strides {x.stride()} on {x.device}")
 
@@ -499,15 +500,15 @@ def _at(x) -> Optional[int]:
 
 def _launch(func, name: str, shape, args, device: int, stream) -> None:
     """Call a C function on the tensors' own GPU and, unless one is given, its current stream."""
-    torch = _t()
+    cuda = _t().cuda
     if stream is None:
-        stream = torch.cuda.current_stream(device).cuda_stream
+        stream = cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(device)
     elif not isinstance(stream, int):
         stream = stream.cuda_stream
-    if device == torch.cuda.current_device():
+    if device == cuda.current_device():
         status = func(ctypes.byref(shape), *args, stream)
     else:
-        with torch.cuda.device(device):
+        with cuda.device(device):
             status = func(ctypes.byref(shape), *args, stream)
     if status != LA_OK:
         raise LaError(status, name)

@@ -255,8 +255,9 @@ __device__ __forceinline__ void widen(float4 a, float4 b, float (&x)[8]) {
 }
 
 // Backward of one batch element's rows; `part`: [B][CTAs][3][C] column sums (sum dy n, sum dy,
-// sum u dh).
-template <typename T, int kThreads>
+// sum u dh). kAll: f, dh and dy are all there (known to the compiler, the row's work is one
+// stretch without branches).
+template <typename T, int kThreads, bool kAll>
 __global__ void __launch_bounds__(kThreads, kThreads == kWide ? 1 : 480 / kThreads)
 norm_backward_kernel(const NormProblem p, const T* x, const T* f, const NormParams w, const T* dh,
                      const T* dy, T* dx, T* df, float* part) {
@@ -270,7 +271,8 @@ norm_backward_kernel(const NormProblem p, const T* x, const T* f, const NormPara
   sm100::pdl_trigger();
   __syncthreads();
   const float inv = 1.0f / static_cast<float>(p.C);
-  const bool has_f = f != nullptr, has_h = dh != nullptr, has_y = dy != nullptr;
+  const bool has_f = kAll || f != nullptr, has_h = kAll || dh != nullptr;
+  const bool has_y = kAll || dy != nullptr;
   const bool post = w.w_post != nullptr;
   int slot = 0;
   float sum_e[KV][8], sum_d[KV][8], sum_f[KV][8];
@@ -279,12 +281,15 @@ norm_backward_kernel(const NormProblem p, const T* x, const T* f, const NormPara
 #pragma unroll
     for (int i = 0; i < 8; ++i) sum_e[k][i] = sum_d[k][i] = sum_f[k][i] = 0.0f;
 
-  // The thread's vectors t and t + width; the second may be missing. Byte offsets in a row, in
-  // the factors, and in the pieces of the next row: [tensor][vector][16 bytes][thread].
+  // The thread's vectors t and t + width. Vectors past the row's end are worked on as zeros (their
+  // pieces stay 0, and they borrow the first vector's factors) but neither loaded nor stored.
+  // Byte offsets in a row, in the factors, and in the pieces of the next row:
+  // [tensor][vector][16 bytes][thread].
   constexpr int kPieces = kVec * sizeof(T) / 16;
   const bool have[KV] = {t < vecs, t + width < vecs};
   const uint32_t base = sm100::smem_u32(smem);
-  const uint32_t m1 = base + t * 16, m2 = m1 + p.C * 4, upper = vecs * 16, next = width * 16;
+  const uint32_t upper = vecs * 16, next = width * 16, line2 = p.C * 4;
+  const uint32_t factor[KV] = {base + (have[0] ? t * 16 : 0), base + (have[1] ? (t + width) * 16 : 0)};
   const uint32_t ahead = base + (2 * p.C + kScratch) * 4 + t * 16;
   const size_t pitch = static_cast<size_t>(p.C) * sizeof(T);
   const size_t move = pitch * gridDim.x;
@@ -312,8 +317,11 @@ norm_backward_kernel(const NormProblem p, const T* x, const T* f, const NormPara
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
+#pragma unroll
+  for (int i = 0; i < 4 * KV * kPieces; ++i)
+    asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(ahead + i * next), "r"(0) : "memory");
   auto take = [&](int a, int k, bool there, float (&out)[8]) {
-    if (there && have[k]) {
+    if (there) {
       const uint32_t at = ahead + (a * KV + k) * kPieces * next;
       const float4 v = lds4(at);
       if (sizeof(T) == 2) {
@@ -330,7 +338,7 @@ norm_backward_kernel(const NormProblem p, const T* x, const T* f, const NormPara
     }
   };
   auto factors = [&](uint32_t line, int k, float (&m)[8]) {
-    widen(lds4(line + k * next), lds4(line + upper + k * next), m);
+    widen(lds4(factor[k] + line), lds4(factor[k] + line + upper), m);
   };
   fetch(blockIdx.x, ofs);
   for (int n = blockIdx.x; n < p.N; n += gridDim.x, ofs += move) {
@@ -359,13 +367,12 @@ norm_backward_kernel(const NormProblem p, const T* x, const T* f, const NormPara
     }
     if (has_f) {
 #pragma unroll
-      for (int k = 0; k < KV; ++k)
-        if (have[k]) {
-          float m[8];
-          factors(m1, k, m);
+      for (int k = 0; k < KV; ++k) {
+        float m[8];
+        factors(0, k, m);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) hx[k][i] = fmaf(u[k][i], m[i], hx[k][i]);
-        }
+        for (int i = 0; i < 8; ++i) hx[k][i] = fmaf(u[k][i], m[i], hx[k][i]);
+      }
     }
     if (has_y) {
       float mean = 0.0f;
@@ -379,31 +386,30 @@ norm_backward_kernel(const NormProblem p, const T* x, const T* f, const NormPara
       }
       float s = 0.0f;
 #pragma unroll
-      for (int k = 0; k < KV; ++k)
-        if (have[k]) {
+      for (int k = 0; k < KV; ++k) {
+        const float centre = have[k] ? mean : 0.0f;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            hx[k][i] -= mean;
-            s = fmaf(hx[k][i], hx[k][i], s);
-          }
+        for (int i = 0; i < 8; ++i) {
+          hx[k][i] -= centre;
+          s = fmaf(hx[k][i], hx[k][i], s);
         }
+      }
       const float rstd = rsqrtf(fmaf(row_sum<kRowWarps>(s, scratch, slot), inv, p.eps));
       float along = 0.0f, off = 0.0f;  // the parts of t = dy w_pre (1 + scale) along n and 1
 #pragma unroll
-      for (int k = 0; k < KV; ++k)
-        if (have[k]) {
-          float m[8];
-          factors(m2, k, m);
+      for (int k = 0; k < KV; ++k) {
+        float m[8];
+        factors(line2, k, m);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            hx[k][i] *= rstd;  // n
-            sum_e[k][i] = fmaf(gy[k][i], hx[k][i], sum_e[k][i]);
-            sum_d[k][i] += gy[k][i];
-            gy[k][i] *= m[i];
-            along = fmaf(gy[k][i], hx[k][i], along);
-            off += gy[k][i];
-          }
+        for (int i = 0; i < 8; ++i) {
+          hx[k][i] *= rstd;  // n
+          sum_e[k][i] = fmaf(gy[k][i], hx[k][i], sum_e[k][i]);
+          sum_d[k][i] += gy[k][i];
+          gy[k][i] *= m[i];
+          along = fmaf(gy[k][i], hx[k][i], along);
+          off += gy[k][i];
         }
+      }
       if (p.layer) {
         row_sum2<kRowWarps>(along, off, scratch, slot);
       } else {
@@ -425,17 +431,16 @@ norm_backward_kernel(const NormProblem p, const T* x, const T* f, const NormPara
     if (!has_f) continue;
     float s = 0.0f;
 #pragma unroll
-    for (int k = 0; k < KV; ++k)
-      if (have[k]) {
-        float m[8];
-        factors(m1, k, m);
+    for (int k = 0; k < KV; ++k) {
+      float m[8];
+      factors(0, k, m);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          sum_f[k][i] = fmaf(u[k][i], g[k][i], sum_f[k][i]);
-          g[k][i] *= m[i];
-          s = fmaf(g[k][i], u[k][i], s);
-        }
+      for (int i = 0; i < 8; ++i) {
+        sum_f[k][i] = fmaf(u[k][i], g[k][i], sum_f[k][i]);
+        g[k][i] *= m[i];
+        s = fmaf(g[k][i], u[k][i], s);
       }
+    }
     if (post) {
       const float part_u = row_sum<kRowWarps>(s, scratch, slot) * inv;
 #pragma unroll
@@ -578,7 +583,9 @@ cudaError_t run_backward(const NormProblem& p, const void* x, const void* f, con
   const int threads = backward_threads(p.C);
   const size_t smem = (2 * static_cast<size_t>(p.C) + kScratch) * sizeof(float) +
                       4 * static_cast<size_t>(threads) * kBackVecs * kVec * sizeof(T);
-  auto kernel = norm_backward_kernel<T, kThreads>;
+  auto kernel = f != nullptr && dh != nullptr && dy != nullptr
+                    ? norm_backward_kernel<T, kThreads, true>
+                    : norm_backward_kernel<T, kThreads, false>;
   const cudaError_t e = allow_smem(kernel, smem);
   if (e != cudaSuccess) return e;
   kernel<<<dim3(static_cast<unsigned>(p.ctas), static_cast<unsigned>(p.B)), threads, smem, s>>>(
