@@ -298,7 +298,7 @@ size_t la_gated_workspace_bytes(const la_gated_shape* shape, int backward);
  * itself, so a sequence can be fed in pieces of any length (prompt, then one
  * token at a time). N = 0 copies S_in to S_out. A NaN or infinity in q, k, v or
  * G may reach the outputs of all tokens of its 16-token block and later ones.
- * float32 sums and state; bf16 outputs are rounded once. Up to 8 tokens run as
+ * float32 sums and state; bf16 outputs are rounded once. Up to 4 tokens run as
  * one launch that walks them one by one; longer calls walk 16-token blocks on
  * the tensor cores, in one launch where B*H fills the GPU, else in three
  * (segments' states, their combination, the segments). Deterministic.

@@ -19,7 +19,8 @@ struct GatedProblem {
   int nseg;     // segments per (batch element, head)
 };
 constexpr int kGateBlock = 16;      // tokens of one tensor-core block
-constexpr int kGateStepTokens = 8;  // up to here tokens are walked one by one
+constexpr int kGateStepTokens = 4;  // up to here tokens are walked one by one (4 tokens of 70 heads:
+                                    // 3.8 us, as a block 4.1 us; 8 tokens: 6.0 us)
 constexpr int kGateAnchor = 256;    // tokens between two stored states of the backward
 
 void gated_split(GatedProblem& p, bool backward);

@@ -829,16 +829,30 @@ cudaError_t backward(const GatedProblem& p, const void* Q, const void* K, const 
 }  // namespace
 }  // namespace gated
 
-// Segments: as many as fill one wave of warps on 148 SMs, none below 64 tokens, where a warp's
-// start and the extra states would cost more than they give. Warps that fit on an SM: by
-// registers (bf16: 168 a thread forwards, 255 backwards) or shared memory (float32).
+// Segments of a row. Cutting costs a second reading of K and V (and Q and dO backwards) and
+// three launches more, so heads that fill half the GPU by themselves are not cut. Otherwise:
+//  - as many segments as give every warp's place on 148 SMs one, by registers (bf16: 168 a
+//    thread forwards, 255 backwards) or shared memory (float32). 16384 tokens of 70 heads, bf16:
+//    100 us, with twice the segments 112 us.
+//  - float32 is bound by its many products, and its warps, more of them, level out better in
+//    four waves: 276 us against 348 us there, 756 against 867 us backwards.
+//  - no segment so short that its start and its state cost more than its work: 64 tokens
+//    (1024 tokens of 36 heads: 10.7 us, with 32 tokens 11.8 us), 96 for much float32 work (8 x
+//    509 tokens of 36 heads: 43 us, with 64 tokens 45 us); where little is to be done at all, the
+//    time is one warp's, and 32 tokens and at most 32 segments are best (256 tokens of 36 heads:
+//    7.0 us, with 64 tokens 8.9 us).
 void gated_split(GatedProblem& p, bool backward) {
-  const long long BH = 1LL * p.B * p.H;
-  const long long per_sm = p.io == LA_IO_BF16 ? (backward ? 8 : 12) : (backward ? 6 : 10);
-  long long n = BH > 0 ? 148LL * per_sm / BH : 1;
+  const long long BH = 1LL * p.B * p.H, work = BH * p.N;
+  const bool bf16 = p.io == LA_IO_BF16;
+  const long long per_sm = bf16 ? (backward ? 8 : 12) : (backward ? 6 : 10);
+  const bool little = work < (backward ? 40000 : 20000);
+  long long n = BH > 0 ? 148 * per_sm / BH : 1;
   if (n < 1) n = 1;
+  if (!bf16 && n > 1) n *= 4;
+  if (little && n > 32) n = 32;
   long long seg = (p.N + n - 1) / n;
-  if (seg < 64) seg = 64;
+  const long long least = little ? 32 : !bf16 && work >= 96000 ? 96 : 64;
+  if (seg < least) seg = least;
   seg = (seg + 31) / 32 * 32;
   p.seg = static_cast<int>(seg);
   p.nseg = p.N > 0 ? static_cast<int>((p.N + seg - 1) / seg) : 1;

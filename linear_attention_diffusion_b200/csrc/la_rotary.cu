@@ -19,8 +19,8 @@
 namespace la {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kFlight = 4;  // items in flight per thread
+constexpr int kThreads = 128;
+constexpr int kFlight = 2;  // items in flight per thread
 enum { kInterleaved = 0, kHalves = 1, kHalvesScalar = 2 };
 
 template <typename T>
@@ -120,14 +120,14 @@ rotary_kernel(const RotaryProblem p, int tokens, const T* q, const T* k, const i
         src[f] = (is_q ? q : k) + ofs;
         dst[f] = (is_q ? qo : ko) + ofs;
         if (kLayout == kInterleaved) {
-          u[f] = *reinterpret_cast<const uint4*>(src[f] + item[f] * V);
+          u[f] = __ldcs(reinterpret_cast<const uint4*>(src[f] + item[f] * V));
         } else if (kLayout == kHalves) {
           const int turning = pairs / V;
           if (item[f] < turning) {
-            u[f] = *reinterpret_cast<const uint4*>(src[f] + item[f] * V);
-            w[f] = *reinterpret_cast<const uint4*>(src[f] + pairs + item[f] * V);
+            u[f] = __ldcs(reinterpret_cast<const uint4*>(src[f] + item[f] * V));
+            w[f] = __ldcs(reinterpret_cast<const uint4*>(src[f] + pairs + item[f] * V));
           } else {
-            u[f] = *reinterpret_cast<const uint4*>(src[f] + p.rot + (item[f] - turning) * V);
+            u[f] = __ldcs(reinterpret_cast<const uint4*>(src[f] + p.rot + (item[f] - turning) * V));
           }
         } else {
           if (item[f] < pairs) {
@@ -156,7 +156,7 @@ rotary_kernel(const RotaryProblem p, int tokens, const T* q, const T* k, const i
             }
           u[f] = pack(x);
         }
-        *reinterpret_cast<uint4*>(dst[f] + item[f] * V) = u[f];
+        __stcs(reinterpret_cast<uint4*>(dst[f] + item[f] * V), u[f]);
       } else if (kLayout == kHalves) {
         const int turning = pairs / V;
         if (item[f] < turning) {
@@ -168,10 +168,10 @@ rotary_kernel(const RotaryProblem p, int tokens, const T* q, const T* k, const i
             const float a = x[j], b = y[j];
             turn(a, b, cs[item[f] * V + j], x[j], y[j]);
           }
-          *reinterpret_cast<uint4*>(dst[f] + item[f] * V) = pack(x);
-          *reinterpret_cast<uint4*>(dst[f] + pairs + item[f] * V) = pack(y);
+          __stcs(reinterpret_cast<uint4*>(dst[f] + item[f] * V), pack(x));
+          __stcs(reinterpret_cast<uint4*>(dst[f] + pairs + item[f] * V), pack(y));
         } else {
-          *reinterpret_cast<uint4*>(dst[f] + p.rot + (item[f] - turning) * V) = u[f];
+          __stcs(reinterpret_cast<uint4*>(dst[f] + p.rot + (item[f] - turning) * V), u[f]);
         }
       } else {
         if (item[f] < pairs) {

@@ -67,7 +67,7 @@ def _forward(case, io, gates, carry, seed=5, scale=0.3):
     _check("S", So, S_ref, AS, tol, HALF["f32"])
 
 
-LENGTHS = [1, 2, 8, 9, 15, 16, 17, 33, 63, 64, 65, 127, 200, 517]
+LENGTHS = [1, 2, 4, 5, 8, 9, 15, 16, 17, 33, 63, 64, 65, 127, 200, 517]
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
