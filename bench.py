@@ -2,7 +2,8 @@
 """Benchmark of one ReLU linear-attention layer on B200.
 
     python bench.py [--gpus N] [--steps K] [--warmup W] [--impl la|reference]
-                    [--workload NAME] [--op layer|reduce|apply|backward|causal|tconv|qkv]
+                    [--workload NAME] [--op layer|reduce|apply|backward|causal|tconv|qkv|
+                                            gated|gated_backward|rotary|norm|norm_backward]
 
 A step is one pass of the layer's hot path over one batch of synthetic input:
 the state reduce (S = sum phi(K)^T V, z = sum ReLU(K)) and the apply
@@ -18,6 +19,10 @@ Both cover the non-causal workloads' shapes. With --op tconv a step is the
 Mix-FFN's temporal depth-wise convolution over the video workload's latent
 grid at the FFN width: a whole clip (sanavideo_480p), or one block reading and
 updating the conv cache (longsana_block_causal).
+--op gated and gated_backward are gated linear attention over the workload's
+tokens and heads; --op rotary turns its queries and keys by one-dimensional
+positions; --op norm and norm_backward are the gated residual with layer norm
+and modulation at the model's hidden width.
 Rank 0 prints one JSON line. Multi-GPU runs are weak-scaled: every rank runs
 its own copy of the workload (heads and batches are independent), with no
 collective on the data path; the time is the max over ranks.
@@ -55,9 +60,14 @@ METRIC_QKV = ("QKV projection + state reduce tokens/s per layer at 1 B200; "
               "achieved TFLOP/s vs bf16 peak")
 METRIC_REDUCE = "linear-attn state-reduce tokens/s per layer at 1 B200; achieved HBM GB/s vs peak"
 METRIC_APPLY = "linear-attn apply tokens/s per layer at 1 B200; achieved HBM GB/s vs peak"
+BLOCK_OPS = {"gated": "gated linear-attn", "gated_backward": "gated linear-attn backward",
+             "rotary": "rotary positions (Q and K)", "norm": "gated residual + layer norm",
+             "norm_backward": "gated residual + layer norm backward"}
 METRICS = {"layer": METRIC, "backward": METRIC_BWD, "causal": METRIC_CAUSAL,
            "tconv": METRIC_TCONV, "qkv": METRIC_QKV, "reduce": METRIC_REDUCE,
            "apply": METRIC_APPLY}
+METRICS.update({op: f"{what} tokens/s per layer at 1 B200; achieved HBM GB/s vs peak"
+                for op, what in BLOCK_OPS.items()})
 # Channels of the temporal convolution: the FFN width of Sana-1.6B, which
 # SANA-Video starts from (width 2240, FFN 5600).
 FFN_WIDTH = 5600
@@ -68,6 +78,7 @@ OP_CONFIG = {"layer": {}, "backward": {"op": "backward (dQ, dK, dV, dS, dz)"},
              "tconv": {"op": "temporal depth-wise conv 3x1x1 + shortcut", "channels": FFN_WIDTH},
              "qkv": {"op": "QKV projection (bf16 GEMM, bias) fused with the state reduce; "
                            "Q out, K and V never leave the chip"}}
+OP_CONFIG.update({op: {"op": what} for op, what in BLOCK_OPS.items()})
 DEFAULT_WORKLOAD = "sanavideo_480p"
 L2_BYTES = 126 * 1024 * 1024
 FALLBACK_HBM_GBS = 6650.0
@@ -628,6 +639,93 @@ def run_tconv(args, w, rank, world, local_rank):
             "per_set_bytes": per_set, "cache_bytes": 0 if cache is None else 2 * per_set // w.T}
 
 
+def run_block_op(args, w, rank, world, local_rank):
+    """Gated attention, rotary positions or the gated residual norm, forward or backward,
+    over the workload's tokens: heads of width 32, or its hidden width."""
+    import torch
+    import linear_attention_diffusion_b200 as la
+
+    dev = torch.device("cuda", local_rank)
+    torch.cuda.set_device(dev)
+    props = torch.cuda.get_device_properties(dev)
+    sampler = ClockSampler(str(getattr(props, "uuid", "") or ""))
+    stream = torch.cuda.Stream(dev)
+    B, N, H, C = w.B, w.N, w.H, wl.hidden_width(w)
+    seed = rank_seed(rank) + 40
+    heads = args.op.startswith("gated") or args.op == "rotary"
+    full = (B, N, H, D) if heads else (B, N, C)
+    n_in = {"gated": 3, "gated_backward": 4, "rotary": 2, "norm": 2, "norm_backward": 4}[args.op]
+    n_out = {"gated": 1, "gated_backward": 3, "rotary": 2, "norm": 2, "norm_backward": 2}[args.op]
+    per_set = n_in * B * N * C * 2
+    n_sets = max(1, min(8, math.ceil(2 * L2_BYTES / per_set)))
+    sets = [[wl.make_tensor(full, seed + 10 * i + j).to(dev) for j in range(n_in)]
+            for i in range(n_sets)]
+    outs = [torch.empty(full, dtype=torch.bfloat16, device=dev) for _ in range(n_out)]
+    extra = 0
+    if args.op.startswith("gated"):
+        G = -0.05 * torch.rand((B, N, H), generator=torch.Generator().manual_seed(seed + 9)).to(dev)
+        dG = torch.empty_like(G)
+        back = args.op == "gated_backward"
+        shape = la.make_gated_shape(B, N, H, scale=D ** -0.5)
+        ws = torch.empty(la.la_gated_workspace_bytes(shape, back), dtype=torch.uint8, device=dev)
+        extra = (2 if back else 1) * G.numel() * 4
+
+        def call(ins, o, st):
+            if back:
+                la.la_gated_attention_backward(shape, *ins[:3], G, None, ins[3], None, *o, dG, None,
+                                               ws, st)
+            else:
+                la.la_gated_attention(shape, *ins, G, None, None, o[0], ws, st)
+        launches = (4 if back else 3) if ws.numel() > 256 else 1
+    elif args.op == "rotary":
+        shape = la.make_rotary_shape(B, N, H, H, D)
+        launches = 1
+
+        def call(ins, o, st):
+            la.la_rotary(shape, ins[0], ins[1], None, o[0], o[1], st)
+    else:
+        par = [wl.make_tensor((B, C), seed + 20 + i, torch.float32).to(dev) for i in range(3)]
+        gate, scale, shift = par
+        w_pre = torch.ones(C, device=dev)
+        shape = la.make_norm_shape(B, N, C)
+        grads = [torch.empty_like(t) for t in (gate, w_pre, scale, shift)]
+        ws = torch.empty(la.la_norm_workspace_bytes(shape), dtype=torch.uint8, device=dev)
+        launches = 2 if args.op == "norm_backward" else 1
+
+        def call(ins, o, st):
+            if args.op == "norm":
+                la.la_gate_residual_norm(shape, *ins, gate, None, w_pre, scale, shift, *o, st)
+            else:
+                la.la_gate_residual_norm_backward(shape, ins[0], ins[1], gate, None, w_pre, scale,
+                                                  ins[2], ins[3], *o, grads[0], None, *grads[1:],
+                                                  ws, st)
+
+    def step(i, evs=None):
+        if evs is not None:
+            evs[0].record(stream)
+        call(sets[i % n_sets], outs, stream)
+        if evs is not None:
+            evs[1].record(stream)
+
+    ms_max, seg_us, chunk, t0, t1 = time_steps(args, step, stream, dev, world, n_sets, False,
+                                               lambda: None)
+    e2e = None
+    if args.e2e_steps > 0:
+        steps = max(1, min(args.steps, args.e2e_steps))
+        hin = [t.cpu().pin_memory() for t in sets[0]]
+        hout = [torch.empty(full, dtype=torch.bfloat16).pin_memory() for _ in range(n_out)]
+        ms = e2e_pipelined(dev, stream, hin, hout, lambda p, ins, o, st: call(ins, o, st), 1, steps)
+        nb = hin[0].numel() * 2
+        e2e = {"ms_per_step": ms, "tokens_per_step": B * N, "steps": steps,
+               "h2d_bytes_per_step": n_in * nb, "d2h_bytes_per_step": n_out * nb,
+               "copies": "pipelined: copy-in, calls and copy-out on three streams, two buffer sets"}
+    clocks = sampler.summary(t0, t1)
+    sampler.stop()
+    return {"ms": ms_max, "seg_us": seg_us, "kernel_names": (args.op,), "e2e": e2e,
+            "clocks": clocks, "launches_per_step": launches, "n_sets": n_sets, "chunk": chunk,
+            "per_set_bytes": per_set, "op_bytes": (n_in + n_out) * B * N * C * 2 + extra}
+
+
 def run_qkv(args, w, rank, world, local_rank):
     """The QKV projection fused with the state reduce, at the model's hidden
     width, with the unfused path (three cuBLAS projections through torch, then
@@ -954,11 +1052,11 @@ def main():
     ap.add_argument("--ref-budget", type=float, default=150.0,
                     help="seconds of oracle work for --impl reference (warm-up and steps)")
     ap.add_argument("--op", choices=["layer", "reduce", "apply", "backward", "causal", "tconv",
-                                     "qkv"],
+                                     "qkv", *BLOCK_OPS],
                     default="layer")
     args = ap.parse_args()
     w = wl.WORKLOADS[args.workload]
-    if args.op in ("backward", "causal", "qkv", "reduce", "apply") and w.block_causal:
+    if args.op in ("backward", "causal", "qkv", "reduce", "apply", *BLOCK_OPS) and w.block_causal:
         ap.error(f"--op {args.op} covers the non-causal workloads")
     if args.op == "tconv" and not w.rope:
         ap.error("--op tconv needs a video workload (sanavideo_480p, longsana_block_causal)")
@@ -969,7 +1067,7 @@ def main():
             per_step_us *= 10
         elif args.op == "tconv":
             per_step_us = 200
-        elif args.op == "qkv":
+        elif args.op == "qkv" or args.op in BLOCK_OPS:
             per_step_us *= 8
         args.steps = max(10, int(0.5e6 / per_step_us))
     args.warmup = max(args.warmup, 3)
@@ -986,8 +1084,8 @@ def main():
         torch.cuda.set_device(local_rank)
         torch.distributed.init_process_group("nccl", timeout=datetime.timedelta(seconds=120),
                                              device_id=torch.device("cuda", local_rank))
-    r = {"tconv": run_tconv, "qkv": run_qkv}.get(args.op, run_la)(args, w, rank, world,
-                                                                  local_rank)
+    run = {"tconv": run_tconv, "qkv": run_qkv, **dict.fromkeys(BLOCK_OPS, run_block_op)}
+    r = run.get(args.op, run_la)(args, w, rank, world, local_rank)
     if world > 1:
         torch.distributed.destroy_process_group()
     if rank != 0:
@@ -999,6 +1097,7 @@ def main():
     peak, peak_src = peaks()
     lb = layer_bytes(w)
     lb["temporal_conv"] = 2 * r["per_set_bytes"] + r.get("cache_bytes", 0)
+    lb[args.op] = r.get("op_bytes", 0)
     # The unit timed is one library call: its average duration is the timed
     # region (back-to-back graph replays, no events between launches) divided
     # by the calls in it. The event graph's per-call figure, which also holds
@@ -1070,6 +1169,11 @@ def main():
                 "la_causal_attention" if args.op == "causal" else
                 "la_temporal_conv" if args.op == "tconv" else
                 "la_qkv_state" if args.op == "qkv" else
+                "la_gate_residual_norm" if args.op == "norm" else
+                "la_gate_residual_norm_backward" if args.op == "norm_backward" else
+                "la_rotary" if args.op == "rotary" else
+                "la_gated_attention" if args.op == "gated" else
+                "la_gated_attention_backward" if args.op == "gated_backward" else
                 "la_block_causal_step" if w.block_causal else "la_attention")}
     out = {"metric": METRICS[args.op], "value": value, "unit": "tokens/s", "n_gpus": world,
            "steps": args.steps, "warmup": args.warmup, "ms_per_step": ms_step,
@@ -1085,7 +1189,7 @@ def main():
         tps, desc, cores, _ = sampler_fn(w, args.cpu_seconds)
         out["cpu_baseline"] = {"value": tps, "unit": "tokens/s", "cores": cores,
                                "kind": "oracle", "sample": desc}
-    elif world == 1 and args.cpu_seconds > 0:
+    elif world == 1 and args.cpu_seconds > 0 and args.op not in BLOCK_OPS:
         tps, desc, cores, _, _ = oracle_sample(w, args.cpu_seconds, op=args.op)
         out["cpu_baseline"] = {"value": tps, "unit": "tokens/s", "cores": cores,
                                "kind": "oracle", "sample": desc}
