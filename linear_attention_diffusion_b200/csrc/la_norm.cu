@@ -83,8 +83,9 @@ struct Line {
     x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
     x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
   }
-  __device__ __forceinline__ float& at(int c) const {
-    return p[((c >> 2) & 1) * 4 * vecs + (c >> 3) * 4 + (c & 3)];
+  __device__ __forceinline__ void put(int v, const float (&x)[8]) const {
+    reinterpret_cast<float4*>(p)[v] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4*>(p)[vecs + v] = make_float4(x[4], x[5], x[6], x[7]);
   }
 };
 
@@ -134,19 +135,38 @@ __device__ __forceinline__ void row_sum2(float& x, float& y, float* scratch, int
   y = across_warps<kWarps>(s + 32);
 }
 
-// Per-channel factors of batch element b: alpha gate w_post, w_pre (1 + scale), shift.
+// Per-channel factors of batch element b: alpha gate w_post, w_pre (1 + scale), shift; eight
+// columns a thread and turn, so that its loads are on their way together.
+__device__ __forceinline__ void load8_or(const float* p, float fill, float (&x)[8]) {
+  if (p != nullptr) {
+    load8(p, x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = fill;
+  }
+}
+template <bool kShift>
 __device__ __forceinline__ void combine_params(const NormProblem& p, const NormParams& w, int b,
-                                               const Line& l1, const Line& l2, const Line* l3) {
+                                               const Line& l1, const Line& l2, const Line& l3) {
   const size_t bc = static_cast<size_t>(b) * p.C;
-  for (int c = threadIdx.x; c < p.C; c += blockDim.x) {
-    float m = p.alpha;
-    if (w.gate != nullptr) m *= w.gate[bc + c];
-    if (w.w_post != nullptr) m *= w.w_post[c];
-    l1.at(c) = m;
-    m = w.w_pre != nullptr ? w.w_pre[c] : 1.0f;
-    if (w.mod_scale != nullptr) m *= 1.0f + w.mod_scale[bc + c];
-    l2.at(c) = m;
-    if (l3 != nullptr) l3->at(c) = w.mod_shift != nullptr ? w.mod_shift[bc + c] : 0.0f;
+  for (int v = threadIdx.x; v < l1.vecs; v += blockDim.x) {
+    const int c = v * kVec;
+    float gate[8], post[8], pre[8], scale[8];
+    load8_or(w.gate != nullptr ? w.gate + bc + c : nullptr, 1.0f, gate);
+    load8_or(w.w_post != nullptr ? w.w_post + c : nullptr, 1.0f, post);
+    load8_or(w.w_pre != nullptr ? w.w_pre + c : nullptr, 1.0f, pre);
+    load8_or(w.mod_scale != nullptr ? w.mod_scale + bc + c : nullptr, 0.0f, scale);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      gate[i] = p.alpha * gate[i] * post[i];
+      pre[i] *= 1.0f + scale[i];
+    }
+    l1.put(v, gate);
+    l2.put(v, pre);
+    if (kShift) {
+      load8_or(w.mod_shift != nullptr ? w.mod_shift + bc + c : nullptr, 0.0f, scale);
+      l3.put(v, scale);
+    }
   }
 }
 
@@ -161,7 +181,7 @@ norm_kernel(const NormProblem p, const T* x, const T* f, const NormParams w, T* 
   float* scratch = smem + 3 * p.C;
   constexpr int kRowWarps = kOneWarp ? 1 : 32;
   for (int i = threadIdx.x; i < kScratch; i += blockDim.x) scratch[i] = 0.0f;
-  combine_params(p, w, b, l1, l2, &l3);
+  combine_params<true>(p, w, b, l1, l2, l3);
   __syncthreads();
   const int width = kOneWarp ? 32 : blockDim.x;  // threads of a row
   const int t = kOneWarp ? threadIdx.x & 31 : threadIdx.x;
@@ -277,10 +297,7 @@ norm_backward_kernel(const NormProblem p, const T* x, const T* f, const NormPara
   const int vecs = p.C / kVec, b = blockIdx.y, t = threadIdx.x, width = blockDim.x;
   const Line l1 = {smem, vecs}, l2 = {smem + p.C, vecs};
   float* scratch = smem + 2 * p.C;
-  for (int i = t; i < kScratch; i += width) scratch[i] = 0.0f;
-  combine_params(p, w, b, l1, l2, nullptr);
   sm100::pdl_trigger();
-  __syncthreads();
   const float inv = 1.0f / static_cast<float>(p.C);
   const bool has_f = kAll || f != nullptr, has_h = kAll || dh != nullptr;
   const bool has_y = kAll || dy != nullptr;
@@ -351,7 +368,10 @@ norm_backward_kernel(const NormProblem p, const T* x, const T* f, const NormPara
   auto factors = [&](uint32_t line, int k, float (&m)[8]) {
     widen(lds4(factor[k] + line), lds4(factor[k] + line + upper), m);
   };
-  fetch(blockIdx.x, ofs);
+  fetch(blockIdx.x, ofs);  // on its way while the factors are combined
+  for (int i = t; i < kScratch; i += width) scratch[i] = 0.0f;
+  combine_params<false>(p, w, b, l1, l2, l2);
+  __syncthreads();
   for (int n = blockIdx.x; n < p.N; n += gridDim.x, ofs += move) {
     float hx[KV][8], u[KV][8], g[KV][8], gy[KV][8];  // h, u / w_post, dh, dy
     asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -477,40 +497,38 @@ norm_backward_kernel(const NormProblem p, const T* x, const T* f, const NormPara
 }
 
 // The parameters' gradients from the CTAs' column sums. blockIdx.y: which of the three sums.
-// 32 columns a CTA; 32 threads per column add the partial sums, always in the same order, of
-// four batch elements at a time (their loads overlap).
-__global__ void __launch_bounds__(1024)
+// 32 columns a CTA, a warp's lanes one each; its warps share up to four batch elements at a
+// time and add the partial sums of each, always in the same order. Two CTAs an SM, so that the
+// three sums of 2240 columns are one wave.
+constexpr int kColumnWarps = 16;
+__global__ void __launch_bounds__(kColumnWarps * 32, 2)
 norm_columns_kernel(const NormProblem p, const NormParams w, const NormGrads g, const float* part) {
-  constexpr int kAtOnce = 4;
-  __shared__ float s[kAtOnce][32][33];
+  __shared__ float s[kColumnWarps][33];
   sm100::pdl_wait();
   const int which = blockIdx.y;
   float* per_b = which == 0 ? g.mod_scale : which == 1 ? g.mod_shift : g.gate;
   float* over_b = which == 0 ? g.w_pre : which == 1 ? nullptr : g.w_post;
   if (per_b == nullptr && over_b == nullptr) return;
-  const int col = threadIdx.x & 31, lane = threadIdx.x >> 5, c = blockIdx.x * 32 + col;
+  const int col = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + col;
+  const int at_once = p.B >= 4 ? 4 : p.B >= 2 ? 2 : 1, share = kColumnWarps / at_once;  // warps
+  const size_t pitch = static_cast<size_t>(3) * p.C;                          // a CTA's sums
   float total = 0.0f;
-  for (int b0 = 0; b0 < p.B; b0 += kAtOnce) {
-    float t[kAtOnce];
-#pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) t[k] = 0.0f;
-    if (c < p.C) {
-#pragma unroll 2
-      for (int i = lane; i < p.ctas; i += 32)
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k)
-          if (b0 + k < p.B)
-            t[k] += __ldcg(part + ((static_cast<size_t>(b0 + k) * p.ctas + i) * 3 + which) * p.C + c);
+  for (int b0 = 0; b0 < p.B; b0 += at_once) {
+    const int b = b0 + warp / share, first = warp % share;
+    float t = 0.0f;
+    if (c < p.C && b < p.B) {
+      const float* at = part + (static_cast<size_t>(b) * p.ctas + first) * pitch +
+                        static_cast<size_t>(which) * p.C + c;
+#pragma unroll 8
+      for (int i = first; i < p.ctas; i += share, at += share * pitch) t += __ldcg(at);
     }
-#pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) s[k][lane][col] = t[k];
+    s[warp][col] = t;
     __syncthreads();
-    // warp k adds up batch element b0 + k; thread (k, col) then has its column's sum
-    if (lane < kAtOnce && b0 + lane < p.B && c < p.C) {
+    // warp k adds up batch element b0 + k: its lane has the column's sum
+    if (warp < at_once && b0 + warp < p.B && c < p.C) {
       float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 32; ++i) sum += s[lane][i][col];
-      const size_t bc = static_cast<size_t>(b0 + lane) * p.C + c;
+      for (int i = 0; i < share; ++i) sum += s[warp * share + i][col];
+      const size_t bc = static_cast<size_t>(b0 + warp) * p.C + c;
       if (which == 0) {  // sum dy n
         if (per_b != nullptr) per_b[bc] = sum * (w.w_pre != nullptr ? w.w_pre[c] : 1.0f);
         if (w.mod_scale != nullptr) sum *= 1.0f + w.mod_scale[bc];
@@ -525,12 +543,11 @@ norm_columns_kernel(const NormProblem p, const NormParams w, const NormGrads g, 
     __syncthreads();
   }
   if (over_b == nullptr) return;
-  if (lane < kAtOnce) s[0][lane][col] = total;
+  if (warp < at_once) s[warp][col] = total;
   __syncthreads();
-  if (lane == 0 && c < p.C) {
+  if (warp == 0 && c < p.C) {
     float sum = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) sum += s[0][k][col];
+    for (int k = 0; k < at_once; ++k) sum += s[k][col];
     over_b[c] = sum;
   }
 }
@@ -651,7 +668,7 @@ cudaError_t launch_norm_backward(const NormProblem& p, const void* x, const void
     return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((p.C + 31) / 32), 3);
-  cfg.blockDim = dim3(1024);
+  cfg.blockDim = dim3(kColumnWarps * 32);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];  // its CTAs may be in place before the sums are done
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
