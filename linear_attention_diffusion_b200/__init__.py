@@ -498,13 +498,22 @@ def _at(x) -> Optional[int]:
     return None if x is None else x.data_ptr()
 
 
-def _launch(func, name: str, shape, args, device: int, stream) -> None:
-    """Call a C function on the tensors' own GPU and, unless one is given, its current stream."""
+def _on(stream, x):
+    """A context with ``stream`` (a torch stream or an address) as the current one of x's GPU, so
+    that outputs and workspaces come from that stream's memory: memory of another stream could
+    be handed out again while a kernel here still uses it."""
+    torch = _t()
+    device = _on_gpu(x)
+    if isinstance(stream, int):
+        stream = (torch.cuda.ExternalStream(stream, device=device) if stream
+                  else torch.cuda.default_stream(device))
+    return torch.cuda.stream(stream)
+
+
+def _launch(func, name: str, shape, args, device: int) -> None:
+    """Call a C function on the tensors' own GPU and its current stream."""
     cuda = _t().cuda
-    if stream is None:
-        stream = cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(device)
-    elif not isinstance(stream, int):
-        stream = stream.cuda_stream
+    stream = cuda.current_stream(device).cuda_stream if _raw_stream is None else _raw_stream(device)
     if device == cuda.current_device():
         status = func(ctypes.byref(shape), *args, stream)
     else:
@@ -547,6 +556,9 @@ def gated_attention(Q, K, V, G, S_in=None, scale: float = 1.0, want_state: bool 
     """O (and the last state when ``want_state`` or ``S_out`` is given) of gated linear attention:
     S_n = exp(g_n) S_{n-1} + k_n^T v_n, o_n = scale q_n S_n, for [B, N, H, 32] CUDA tensors and
     log gates G [B, N, H] float32. ``S_out`` may be ``S_in``: the state is then updated in place."""
+    if stream is not None:
+        with _on(stream, Q):
+            return gated_attention(Q, K, V, G, S_in, scale, want_state, S_out)
     torch = _t()
     shape = _gated_shape(Q, K, V, G, scale, S_in=S_in, S_out=S_out)
     device = _on_gpu(Q)
@@ -558,7 +570,7 @@ def gated_attention(Q, K, V, G, S_in=None, scale: float = 1.0, want_state: bool 
     ws, n = _scratch(n, Q) if n > 256 else (None, 0)
     _launch(_lib.la_gated_attention, "la_gated_attention", shape,
             (Q.data_ptr(), K.data_ptr(), V.data_ptr(), G.data_ptr(), _at(S_in), _at(S_out), O.data_ptr(),
-             _at(ws), n), device, stream)
+             _at(ws), n), device)
     return O if S_out is None else (O, S_out)
 
 
@@ -566,6 +578,9 @@ def gated_attention_backward(Q, K, V, G, dO, S_in=None, dS_out=None, scale: floa
                              want_state: Optional[bool] = None, stream=None):
     """dQ, dK, dV, dG, dS_in of gated_attention. dS_in is None unless ``want_state`` (by default:
     where an S_in is given); S_in must still hold the state that the forward began with."""
+    if stream is not None:
+        with _on(stream, Q):
+            return gated_attention_backward(Q, K, V, G, dO, S_in, dS_out, scale, want_state)
     torch = _t()
     shape = _gated_shape(Q, K, V, G, scale, S_in=S_in, dS_out=dS_out)
     _need("dO", dO, Q.shape, Q.dtype, Q.get_device())
@@ -579,7 +594,7 @@ def gated_attention_backward(Q, K, V, G, dO, S_in=None, dS_out=None, scale: floa
     ws, n = _scratch(_lib.la_gated_workspace_bytes(ctypes.byref(shape), 1), Q)
     _launch(_lib.la_gated_attention_backward, "la_gated_attention_backward", shape,
             (Q.data_ptr(), K.data_ptr(), V.data_ptr(), G.data_ptr(), _at(S_in), dO.data_ptr(), _at(dS_out),
-             dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), dG.data_ptr(), _at(dS), _at(ws), n), device, stream)
+             dQ.data_ptr(), dK.data_ptr(), dV.data_ptr(), dG.data_ptr(), _at(dS), _at(ws), n), device)
     return dQ, dK, dV, dG, dS
 
 
@@ -613,6 +628,9 @@ def rotary(Q, K=None, positions=None, offset: int = 0, rot: Optional[int] = None
     ``positions``: int32 [N] or [B, N], or None for offset + n. ``rot``: dimensions that turn
     (default: all). ``inverse`` turns back, which is the gradient. ``out``: (Qo, Ko), which may be
     (Q, K) to work in place. Frequencies and ``scaling``: see make_rotary_shape and include/la.h."""
+    if stream is not None:
+        with _on(stream, Q):
+            return rotary(Q, K, positions, offset, rot, layout, base, scaling, mscale, inverse, out)
     torch = _t()
     if Q.dim() != 4:
         raise ValueError(f"Q must be [B, N, H, D], got {tuple(Q.shape)}")
@@ -641,7 +659,7 @@ def rotary(Q, K=None, positions=None, offset: int = 0, rot: Optional[int] = None
     elif Ko is None:
         Ko = torch.empty_like(K)
     _launch(_lib.la_rotary, "la_rotary", shape,
-            (Q.data_ptr(), _at(K), _at(positions), Qo.data_ptr(), _at(Ko)), device, stream)
+            (Q.data_ptr(), _at(K), _at(positions), Qo.data_ptr(), _at(Ko)), device)
     return Qo, Ko
 
 
@@ -677,6 +695,10 @@ def gate_residual_norm(x, f=None, gate=None, w_post=None, w_pre=None, mod_scale=
     with float32 parameters gate, mod_scale, mod_shift [B, C] and w_post, w_pre [C]. h is None
     without f or with ``want_h=False``, y with ``want_y=False``. ``out``: (h, y), each of which
     may be x or f."""
+    if stream is not None:
+        with _on(stream, x):
+            return gate_residual_norm(x, f, gate, w_post, w_pre, mod_scale, mod_shift, norm, eps, alpha,
+                                      out, want_h, want_y)
     torch = _t()
     h, y = (None, None) if out is None else out
     shape = _norm_shape(x, f, gate, w_post, w_pre, mod_scale, mod_shift, norm, eps, alpha, h=h, y=y)
@@ -687,7 +709,7 @@ def gate_residual_norm(x, f=None, gate=None, w_post=None, w_pre=None, mod_scale=
         y = torch.empty_like(x)
     _launch(_lib.la_gate_residual_norm, "la_gate_residual_norm", shape,
             (x.data_ptr(), _at(f), _at(gate), _at(w_post), _at(w_pre), _at(mod_scale), _at(mod_shift),
-             _at(h), _at(y)), device, stream)
+             _at(h), _at(y)), device)
     return h, y
 
 
@@ -696,6 +718,10 @@ def gate_residual_norm_backward(x, f, dy, dh, gate=None, w_post=None, w_pre=None
                                 alpha: float = 1.0, stream=None):
     """dx, df, dgate, dw_post, dw_pre, dmod_scale, dmod_shift of gate_residual_norm: None for what
     was not given (dmod_shift with mod_shift). f, and one of dy and dh, may be None."""
+    if stream is not None:
+        with _on(stream, x):
+            return gate_residual_norm_backward(x, f, dy, dh, gate, w_post, w_pre, mod_scale,
+                                               mod_shift, norm, eps, alpha)
     torch = _t()
     shape = _norm_shape(x, f, gate, w_post, w_pre, mod_scale, mod_shift, norm, eps, alpha, dy=dy, dh=dh)
     device = _on_gpu(x)
@@ -704,5 +730,5 @@ def gate_residual_norm_backward(x, f, dy, dh, gate=None, w_post=None, w_pre=None
     ws, n = _scratch(_lib.la_norm_workspace_bytes(ctypes.byref(shape)), x)
     _launch(_lib.la_gate_residual_norm_backward, "la_gate_residual_norm_backward", shape,
             (x.data_ptr(), _at(f), _at(gate), _at(w_post), _at(w_pre), _at(mod_scale), _at(dh), _at(dy),
-             *(_at(g) for g in grads), _at(ws), n), device, stream)
+             *(_at(g) for g in grads), _at(ws), n), device)
     return tuple(grads)

@@ -237,3 +237,53 @@ def test_later_tokens_and_other_rows_do_not_reach_earlier_ones(cuda_device):
     ws = torch.empty(la.la_gated_workspace_bytes(shape), dtype=torch.uint8, device="cuda")
     la.la_gated_attention(shape, *dev, None, None, out, ws)
     assert torch.equal(out, la.gated_attention(*dev)) and bool((buf[B * N * H * D:] == 7.0).all())
+
+
+def test_stream_argument(cuda_device):
+    """Calls on a stream that is not the current one, its memory its own: many calls whose
+    results are dropped at once, and one that is kept."""
+    q, k, v, g, do, S, dS = _dev(*_draw(2, 700, 5, "bf16", 8))
+    want = [*la.gated_attention(q, k, v, g, S_in=S, want_state=True),
+            *la.gated_attention_backward(q, k, v, g, do, S_in=S, dS_out=dS)]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for stream in (s, s.cuda_stream):
+        for _ in range(5):
+            la.gated_attention_backward(q, k, v, g, do, stream=stream)
+            torch.full((1 << 22,), 7.0, device="cuda")  # the current stream's allocations meanwhile
+        got = [*la.gated_attention(q, k, v, g, S_in=S, want_state=True, stream=stream),
+               *la.gated_attention_backward(q, k, v, g, do, S_in=S, dS_out=dS, stream=stream)]
+        s.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.slow
+def test_tensors_past_32_bit_offsets(cuda_device):
+    """2.2e9 elements a tensor. A stop a few tokens before the end leaves the oracle a short
+    sequence; the last heads are the farthest in memory."""
+    B, N, H, tail = 1, 67200, 1024, 40
+    if torch.cuda.get_device_properties(0).total_memory < 100 << 30:
+        pytest.skip("needs 60 GB")
+    r = torch.Generator(device="cuda").manual_seed(5)
+    q, k, v, do = (torch.randn((B, N, H, D), generator=r, device="cuda", dtype=torch.bfloat16) for _ in range(4))
+    g = -0.1 * torch.rand((B, N, H), generator=r, device="cuda")
+    g[:, N - tail] = -float("inf")
+    cut = [x[:, N - tail:, H - 3:].contiguous().cpu() for x in (q, k, v, g, do)]
+    O, S = la.gated_attention(q, k, v, g, scale=0.3, want_state=True)
+    ref, S_ref = orc.gated_attention(*cut[:4], scale=0.3)
+    A, AS = orc.gated_magnitudes(*cut[:4], scale=0.3)
+    _check("O", O[:, N - tail:, H - 3:], ref, A, _tol("bf16", tail), HALF["bf16"])
+    _check("S", S[:, H - 3:], S_ref, AS, _tol("bf16", tail), HALF["f32"])
+    del O, S
+    grads = la.gated_attention_backward(q, k, v, g, do, scale=0.3)
+    refs = orc.gated_attention_backward(*cut, scale=0.3)
+    mags = orc.gated_magnitudes(*cut, scale=0.3)
+    for i, name in enumerate(("dQ", "dK", "dV", "dG")):
+        _check(name, grads[i][:, N - tail:, H - 3:], refs[i], mags[i], 2 * _tol("bf16", tail),
+               HALF["bf16" if i < 3 else "f32"])
+    del grads, v, do, g
+    Qo, Ko = la.rotary(q, k, out=(q, k))
+    for x, src in ((Qo, cut[0]), (Ko, cut[1])):
+        want = orc.rotary(src, np.arange(N - tail, N), D)
+        err = np.abs(orc.to_f64(x[:, N - tail:, H - 3:].cpu()) - want)
+        assert (err <= HALF["bf16"] * np.abs(want) + 2.0 ** -20 * 8).all()
