@@ -297,7 +297,9 @@ size_t la_gated_workspace_bytes(const la_gated_shape* shape, int backward);
  * zero state. S_out (may be NULL) receives the last state; it may be S_in
  * itself, so a sequence can be fed in pieces of any length (prompt, then one
  * token at a time). N = 0 copies S_in to S_out. A NaN or infinity in q, k, v or
- * G may reach the outputs of all tokens of its 16-token block and later ones.
+ * G may reach the outputs of all tokens of its 16-token block and of later ones (in the
+ * backward also of earlier ones); a gate that lets nothing through ends that, but only
+ * from the next 32 tokens on.
  * float32 sums and state; bf16 outputs are rounded once. Up to 4 tokens run as
  * one launch that walks them one by one; longer calls walk 16-token blocks on
  * the tensor cores, in one launch where B*H fills the GPU, else in three
@@ -379,7 +381,8 @@ typedef struct {
  *                                             (w_pre [C], mod_* [B, C]; NULL: 1, 0, 0)
  * f may be NULL (then gate, w_post and h must be): a plain norm with modulation. y or h
  * may be NULL where it is not wanted, not both. h may be x or f, and y may be x or f,
- * exactly; no other overlap is allowed, and h is not y. The norm of y is taken of h
+ * exactly; no other overlap is allowed, and h is not y. With eps = 0 a row of zeros gives
+ * NaN, as the formula does. The norm of y is taken of h
  * before its rounding. float32 arithmetic, each output rounded once. One launch. */
 la_status la_gate_residual_norm(const la_norm_shape* shape, const void* x, const void* f,
                                 const float* gate, const float* w_post, const float* w_pre,

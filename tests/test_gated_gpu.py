@@ -287,3 +287,25 @@ def test_tensors_past_32_bit_offsets(cuda_device):
         want = orc.rotary(src, np.arange(N - tail, N), D)
         err = np.abs(orc.to_f64(x[:, N - tail:, H - 3:].cpu()) - want)
         assert (err <= HALF["bf16"] * np.abs(want) + 2.0 ** -20 * 8).all()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("N,bad,stop", [(3000, 700, 740), (200, 5, 40), (300, 0, 64)])
+def test_a_stop_ends_what_is_not_finite(cuda_device, io, N, bad, stop):
+    """NaN and infinity in one sequence reach neither the tokens before their block nor, 32
+    tokens after the next one's start, the sequence packed behind it, whichever way the row
+    is cut into segments."""
+    q, k, v, g, do, _, _ = _draw(1, N, 3, io, 17, carry=False)
+    g[:, stop] = -float("inf")
+    v[:, bad, 1] = float("nan")
+    k[:, bad, 2] = float("inf")
+    O, S = la.gated_attention(*_dev(q, k, v, g), want_state=True)
+    tail = [x[:, stop:] for x in (q, k, v, g)]
+    ref, S_ref = orc.gated_attention(*tail)
+    A, AS = orc.gated_magnitudes(*tail)
+    _check("O", O[:, stop + 32:], ref[:, 32:], A[:, 32:], _tol(io, N), HALF[io])
+    _check("S", S, S_ref, AS, _tol(io, N), HALF["f32"])
+    first = bad // 16 * 16
+    ref, _ = orc.gated_attention(*(x[:, :first] for x in (q, k, v, g)))
+    A, _ = orc.gated_magnitudes(*(x[:, :first] for x in (q, k, v, g)))
+    _check("O before", O[:, :first], ref, A, _tol(io, N), HALF[io])
