@@ -302,8 +302,8 @@ size_t la_gated_workspace_bytes(const la_gated_shape* shape, int backward);
  * from the next 32 tokens on.
  * float32 sums and state; bf16 outputs are rounded once. Up to 4 tokens run as
  * one launch that walks them one by one; longer calls walk 16-token blocks on
- * the tensor cores, in one launch where B*H fills the GPU, else in three
- * (segments' states, their combination, the segments). Deterministic.
+ * the tensor cores, in one launch where the rows are short or B*H fills the GPU,
+ * else in three (segments' states, their combination, the segments). Deterministic.
  * O must not overlap an input, S_out or the workspace; S_out must not overlap
  * an input other than being S_in, nor the workspace. */
 la_status la_gated_attention(const la_gated_shape* shape, const void* Q, const void* K,

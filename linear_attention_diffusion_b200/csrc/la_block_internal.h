@@ -17,6 +17,7 @@ struct GatedProblem {
   float scale;  // applied to the queries
   int seg;      // tokens of one warp's segment, a multiple of 32
   int nseg;     // segments per (batch element, head)
+  bool whole_row;  // forwards: a CTA takes all segments of a head in one launch
 };
 constexpr int kGateBlock = 16;      // tokens of one tensor-core block
 constexpr int kGateStepTokens = 4;  // up to here tokens are walked one by one (4 tokens of 70 heads:

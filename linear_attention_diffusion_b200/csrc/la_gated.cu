@@ -143,41 +143,28 @@ __device__ __forceinline__ void block_row(float (&acc)[4][4], int b, const Frag<
 // writes q . dq of every token and S at the anchors.
 // kExact: the state's own update keeps 24 bits, for a state that goes out in float32 or stands
 // behind a float32 gradient; else 17, as many as a bf16 output can show.
-template <int NP, bool kBack, bool kExact, int kStages>
-__global__ void __launch_bounds__(kWarps<NP> * 32, kBack ? (NP == 1 ? 2 : 4) : NP == 1 ? 3 : 5)
-walk_kernel(const Walk a) {
+// `smem`: the warp's shared memory; start(S) sets the state at the segment's start, once the
+// first copies are on their way; S is left as it is at the segment's end.
+template <int NP, bool kBack, bool kExact, int kStages, typename Start>
+__device__ __forceinline__ void walk_pass(const Walk& a, const Place<kBlocks<NP>>& at, uint32_t smem,
+                                          int lane, State& S, const Start& start) {
   using T = typename Io<NP>::T;
   constexpr int NB = kBlocks<NP>, NT = kBack ? 4 : 3, NC = parts(NP, kBack);
   constexpr int kStep = NB * kGateBlock;
   using M = Smem<NP, NB, NT, kStages, 3>;
-  extern __shared__ __align__(128) uint8_t smem_all[];
   const GatedProblem& p = a.p;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long unit = static_cast<long long>(blockIdx.x) * kWarps<NP> + warp;
-  if (unit >= static_cast<long long>(p.B) * p.H * p.nseg) return;
-  const Place<NB> at(p, unit);
   const T* heads[NT];
   heads[0] = static_cast<const T*>(a.q) + at.base;
   heads[1] = static_cast<const T*>(a.k) + at.base;
   heads[2] = static_cast<const T*>(a.v) + at.base;
   if (kBack) heads[NT - 1] = static_cast<const T*>(a.w) + at.base;
-  const uint32_t smem = smem_addr(smem_all) + warp * M::kWarp;
   const uint32_t planes = smem + kStages * M::kStage;
   Ring<NP, NB, NT, kStages, 3, false, false> ring(smem, heads, a.G + at.gbase, p.H, nullptr,
                                                   at.n_begin, at.n_end, at.iters, lane);
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) ring.issue(lane);
   Out<NP> out(a.o, at.base, p.H, at.n_begin, lane);
-  sm100::pdl_trigger();
-  sm100::pdl_wait();  // the inputs were there before; the states come from the kernel before
-
-  State S;
-  if (p.nseg > 1)
-    S.load(a.prefix + (static_cast<size_t>(at.bh) * p.nseg + at.seg) * 1024, lane);
-  else if (a.init != nullptr)
-    S.template load_outer<!kBack>(a.init + static_cast<size_t>(at.bh) * 1024, lane);
-  else
-    S.zero();
+  start(S);
   float* anchors = nullptr;
   if (kBack)
     anchors = a.anchors + (static_cast<size_t>(at.bh) * (p.nseg * a.per_seg + 1) +
@@ -275,12 +262,34 @@ walk_kernel(const Walk a) {
       step(Const<false>());
   }
   cp_wait<0>();
-  if (at.seg == p.nseg - 1) {
-    if (!kBack && a.final_ != nullptr)
-      S.template store_outer<true>(a.final_ + static_cast<size_t>(at.bh) * 1024, lane);
-    if (kBack)  // the state after the last token: the anchor of the row's end
-      S.store(anchors + static_cast<size_t>(a.per_seg) * 1024, lane);
-  }
+  if (kBack && at.seg == p.nseg - 1)  // the state after the last token: the anchor of the row's end
+    S.store(anchors + static_cast<size_t>(a.per_seg) * 1024, lane);
+}
+
+template <int NP, bool kBack, bool kExact, int kStages>
+__global__ void __launch_bounds__(kWarps<NP> * 32, kBack ? (NP == 1 ? 2 : 4) : NP == 1 ? 3 : 5)
+walk_kernel(const Walk a) {
+  extern __shared__ __align__(128) uint8_t smem_all[];
+  const GatedProblem& p = a.p;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long unit = static_cast<long long>(blockIdx.x) * kWarps<NP> + warp;
+  if (unit >= static_cast<long long>(p.B) * p.H * p.nseg) return;
+  const Place<kBlocks<NP>> at(p, unit);
+  State S;
+  walk_pass<NP, kBack, kExact, kStages>(
+      a, at, smem_addr(smem_all) + warp * Smem<NP, kBlocks<NP>, kBack ? 4 : 3, kStages, 3>::kWarp,
+      lane, S, [&](State& s) {
+        sm100::pdl_trigger();
+        sm100::pdl_wait();  // the inputs were there before; the states come from the kernel before
+        if (p.nseg > 1)
+          s.load(a.prefix + (static_cast<size_t>(at.bh) * p.nseg + at.seg) * 1024, lane);
+        else if (a.init != nullptr)
+          s.template load_outer<!kBack>(a.init + static_cast<size_t>(at.bh) * 1024, lane);
+        else
+          s.zero();
+      });
+  if (!kBack && a.final_ != nullptr && at.seg == p.nseg - 1)
+    S.template store_outer<true>(a.final_ + static_cast<size_t>(at.bh) * 1024, lane);
 }
 
 // One segment backwards: dk and dv (o and o2), the log gates' gradient, and with
@@ -466,19 +475,14 @@ walk_back_kernel(const Walk a) {
 // segments' first tokens, the walk reads first, while it is still in L2. Once the decay to
 // the segment's end has become 0, no earlier token has a part in S.
 template <int NP, bool kBack, int kStages>
-__global__ void __launch_bounds__(kWarps<NP> * 32, kBack ? (NP == 1 ? 2 : 4) : NP == 1 ? 4 : 5)
-segment_kernel(const GatedProblem p, int segs, const void* qv, const void* kv, const void* vv,
-               const void* dov, const float* Gv, float* states, float* last_states, float* grads,
-               float* decays) {
+__device__ __forceinline__ void segment_pass(const GatedProblem& p, const Place<kBlocks<NP>>& at,
+                                             const void* qv, const void* kv, const void* vv,
+                                             const void* dov, const float* Gv, uint32_t smem,
+                                             int lane, State& S, State& X, float& total) {
   using T = typename Io<NP>::T;
   constexpr int NB = kBlocks<NP>, NT = kBack ? 4 : 2;
   constexpr int kStep = NB * kGateBlock;
   using M = Smem<NP, NB, NT, kStages>;
-  extern __shared__ __align__(128) uint8_t smem_all[];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const long long unit = static_cast<long long>(blockIdx.x) * kWarps<NP> + warp;
-  if (unit >= static_cast<long long>(p.B) * p.H * segs) return;
-  const Place<NB> at(p, unit);
   const T* heads[NT];
   heads[0] = static_cast<const T*>(kBack ? kv : vv) + at.base;
   heads[1] = static_cast<const T*>(kBack ? vv : kv) + at.base;
@@ -486,18 +490,15 @@ segment_kernel(const GatedProblem p, int segs, const void* qv, const void* kv, c
     heads[NT - 2] = static_cast<const T*>(qv) + at.base;
     heads[NT - 1] = static_cast<const T*>(dov) + at.base;
   }
-  sm100::pdl_trigger();
-  const uint32_t smem = smem_addr(smem_all) + warp * M::kWarp;
   const uint32_t planes = smem + kStages * M::kStage;
   Ring<NP, NB, NT, kStages, NT, true, false> ring(smem, heads, Gv + at.gbase, p.H, nullptr,
                                                   at.n_begin + (at.iters - 1) * kStep, at.n_end,
                                                   at.iters, lane);
 #pragma unroll
   for (int i = 0; i < kStages - 1; ++i) ring.issue(lane);
-  State S, X;
   S.zero();
   if (kBack) X.zero();
-  float total = 1.0f;
+  total = 1.0f;
   const LaneOff off(lane);
   for (int it = 0; it < at.iters; ++it) {
     const uint32_t st = ring.next(lane);
@@ -556,6 +557,26 @@ segment_kernel(const GatedProblem p, int segs, const void* qv, const void* kv, c
     if (!kBack && total == 0.0f) break;
   }
   cp_wait<0>();
+  __syncwarp();  // the stages are free
+}
+
+template <int NP, bool kBack, int kStages>
+__global__ void __launch_bounds__(kWarps<NP> * 32, kBack ? (NP == 1 ? 2 : 4) : NP == 1 ? 4 : 5)
+segment_kernel(const GatedProblem p, int segs, const void* qv, const void* kv, const void* vv,
+               const void* dov, const float* Gv, float* states, float* last_states, float* grads,
+               float* decays) {
+  extern __shared__ __align__(128) uint8_t smem_all[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long unit = static_cast<long long>(blockIdx.x) * kWarps<NP> + warp;
+  if (unit >= static_cast<long long>(p.B) * p.H * segs) return;
+  const Place<kBlocks<NP>> at(p, unit);
+  sm100::pdl_trigger();
+  State S, X;
+  float total;
+  segment_pass<NP, kBack, kStages>(
+      p, at, qv, kv, vv, dov, Gv,
+      smem_addr(smem_all) + warp * Smem<NP, kBlocks<NP>, kBack ? 4 : 2, kStages>::kWarp, lane, S, X,
+      total);
   const size_t slots = static_cast<size_t>(at.bh) * p.nseg;
   if (at.seg + 1 < p.nseg)
     S.store(states + (slots + at.seg + 1) * 1024, lane);
@@ -563,6 +584,55 @@ segment_kernel(const GatedProblem p, int segs, const void* qv, const void* kv, c
     S.store(last_states + static_cast<size_t>(at.bh) * 1024, lane);
   if (kBack && at.seg > 0) X.store(grads + (slots + at.seg - 1) * 1024, lane);
   if (lane == 0) decays[slots + at.seg] = total;
+}
+
+// A whole row in one CTA: its warps take the segments of one head, leave the segments' own
+// states in shared memory, and each adds up those before its own. K and V come from L2 the
+// second time, and nothing of a second or third launch is left. Four warps: 8 x 509 tokens of
+// 36 heads in bf16 take 15.3 us (two warps 19.6, six 15.8, three launches 20.5).
+constexpr int kRowWarps = 4;
+template <int NP>
+struct RowSmem {
+  static constexpr int kStages = 2;
+  using M = Smem<NP, kBlocks<NP>, 3, kStages, 3>;  // the walk's; the first pass needs less
+  static_assert(Smem<NP, kBlocks<NP>, 2, kStages>::kWarp <= M::kWarp, "the first pass's ring fits");
+  static constexpr int kState = 4096 + 16;  // and the segment's decay
+  static constexpr int kWarp = M::kWarp + kState;
+};
+
+template <int NP>
+__global__ void __launch_bounds__(kRowWarps * 32, NP == 1 ? 3 : 2) row_kernel(const Walk a) {
+  using R = RowSmem<NP>;
+  extern __shared__ __align__(128) uint8_t smem_all[];
+  const GatedProblem& p = a.p;
+  const int lane = threadIdx.x & 31, seg = threadIdx.x >> 5;
+  const long long BH = static_cast<long long>(p.B) * p.H;
+  const Place<kBlocks<NP>> at(p, seg * BH + blockIdx.x);
+  const uint32_t smem = smem_addr(smem_all) + seg * R::M::kWarp;
+  const uint32_t states = smem_addr(smem_all) + p.nseg * R::M::kWarp;  // [nseg] states, then decays
+  const uint32_t decays = states + p.nseg * 4096;
+  const float* init = a.init != nullptr ? a.init + static_cast<size_t>(at.bh) * 1024 : nullptr;
+  State S, first;
+  float total;
+  segment_pass<NP, false, R::kStages>(p, at, nullptr, a.k, a.v, nullptr, a.G, smem, lane, S, first,
+                                      total);
+  first.zero();
+  if (seg == 0 && init != nullptr) {  // read by this warp alone, before the last one writes
+    first.template load_outer<true>(init, lane);
+    if (total != 0.0f) S.add_scaled(first, total);
+  }
+  S.put(states + seg * 4096, lane);
+  if (lane == 0) sts(decays + seg * 4, __float_as_uint(total));
+  walk_pass<NP, false, NP == 3, R::kStages>(a, at, smem, lane, S, [&](State& s) {
+    __syncthreads();
+    s = first;  // of segment 0; the others' starts from zero
+    for (int i = 0; i < seg; ++i) s.follow(states + i * 4096, lds(decays + i * 4), lane);
+    if (a.final_ != nullptr && seg == p.nseg - 1) {
+      State end = s;
+      end.follow(states + seg * 4096, seg == 0 ? 0.0f : total, lane);
+      end.template store_outer<true>(a.final_ + static_cast<size_t>(at.bh) * 1024, lane);
+    }
+  });
 }
 
 // Segments in order: slot s becomes the state at segment s's start (forwards), or the
@@ -754,6 +824,19 @@ cudaError_t forward(const GatedProblem& p, const void* Q, const void* K, const v
   float* last_states = states + BH * p.nseg * 1024;
   float* decays = last_states + BH * 1024;
   cudaError_t e;
+  Walk a = {};
+  a.q = Q;
+  a.k = K;
+  a.v = V;
+  a.G = G;
+  a.o = O;
+  a.init = S_in;
+  a.p = p;
+  if (p.whole_row) {
+    a.final_ = S_out;
+    return launch(row_kernel<NP>, dim3(static_cast<unsigned>(BH)), p.nseg * 32,
+                  p.nseg * RowSmem<NP>::kWarp, false, s, a);
+  }
   if (p.nseg > 1) {
     const int segs = S_out != nullptr ? p.nseg : p.nseg - 1;
     e = launch(segment_kernel<NP, false, kSegStages>, grid_of<NP>(BH * segs), kWarps<NP> * 32,
@@ -764,16 +847,8 @@ cudaError_t forward(const GatedProblem& p, const void* Q, const void* K, const v
                decays, states, S_in, nullptr, nullptr, last_states, S_out);
     if (e != cudaSuccess) return e;
   }
-  Walk a = {};
-  a.q = Q;
-  a.k = K;
-  a.v = V;
-  a.G = G;
-  a.o = O;
-  a.init = S_in;
   a.final_ = p.nseg > 1 ? nullptr : S_out;
   a.prefix = states;
-  a.p = p;
   auto walk = walk_kernel<NP, false, true, kStages>;
   if constexpr (NP == 1) {
     if (a.final_ == nullptr) walk = walk_kernel<NP, false, false, kStages>;
@@ -851,6 +926,13 @@ cudaError_t backward(const GatedProblem& p, const void* Q, const void* K, const 
 //    509 tokens of 36 heads: 43 us, with 64 tokens 45 us); where little is to be done at all, the
 //    time is one warp's, and 32 tokens and at most 32 segments are best (256 tokens of 36 heads:
 //    7.0 us, with 64 tokens 8.9 us).
+//
+// Forwards, a CTA takes a whole row where its four warps are enough: short rows, or rows of
+// so many heads that they would not be cut much finer. In one launch against three, bf16: 256
+// tokens of 70 heads 6.9 and 7.6 us (512 tokens: 10.9 and 10.0), 1024 tokens of 140 heads 19.2
+// and 21.1 us (2048: 35.8 and 33.9), 2000 tokens of 630 heads 132 and 144 us (4096 of 280: 111
+// and 103). float32, whose warps are fewer: 1024 tokens of 280 heads 70 and 76 us (of 140: 47 and
+// 46), 64 tokens 9.0 and 12.0 us; more heads than one wave of CTAs: 333 and 285 us (630 heads).
 void gated_split(GatedProblem& p, bool backward) {
   const long long BH = 1LL * p.B * p.H, work = BH * p.N;
   const bool bf16 = p.io == LA_IO_BF16;
@@ -866,12 +948,20 @@ void gated_split(GatedProblem& p, bool backward) {
   seg = (seg + 31) / 32 * 32;
   p.seg = static_cast<int>(seg);
   p.nseg = p.N > 0 ? static_cast<int>((p.N + seg - 1) / seg) : 1;
+  p.whole_row = !backward && n > 1 && p.N > 0 &&
+                (bf16 ? p.N <= 256 || (BH >= 128 && p.N <= 1024) || (BH >= 256 && p.N <= 2048)
+                      : BH <= 296 && (p.N <= 128 || (BH >= 200 && p.N <= 2048)));
+  if (p.whole_row) {
+    seg = ((p.N + gated::kRowWarps - 1) / gated::kRowWarps + 31) / 32 * 32;
+    p.seg = static_cast<int>(seg);
+    p.nseg = static_cast<int>((p.N + seg - 1) / seg);
+  }
 }
 
 size_t gated_workspace_floats(const GatedProblem& p, bool backward) {
   const size_t BH = static_cast<size_t>(p.B) * p.H;
   const size_t states = BH * p.nseg * 1024, decays = BH * p.nseg;
-  if (!backward) return p.nseg > 1 ? states + BH * 1024 + decays : 0;
+  if (!backward) return p.nseg > 1 && !p.whole_row ? states + BH * 1024 + decays : 0;
   const size_t anchors = BH * (static_cast<size_t>(p.nseg) * gated::gated_anchors(p) + 1) * 1024;
   return 2 * states + anchors + (BH * p.N + 3) / 4 * 4 + decays;
 }

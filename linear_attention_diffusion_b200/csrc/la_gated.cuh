@@ -126,6 +126,36 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Float `i` of shared memory at `addr`.
+__device__ __forceinline__ float lds(uint32_t addr) {
+  float x;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+  return x;
+}
+__device__ __forceinline__ uint2 lds2(uint32_t addr) {
+  uint2 x;
+  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(addr) : "memory");
+  return x;
+}
+__device__ __forceinline__ uint4 lds4(uint32_t addr) {
+  uint4 x;
+  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "r"(addr)
+               : "memory");
+  return x;
+}
+__device__ __forceinline__ void sts(uint32_t addr, uint32_t x) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
+}
+__device__ __forceinline__ void sts2(uint32_t addr, float x, float y) {
+  asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
+}
+__device__ __forceinline__ void sts4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w)
+               : "memory");
+}
+
 // Packed bf16 arithmetic, each result rounded once.
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   uint32_t d;
@@ -320,6 +350,38 @@ struct State {
       for (int nt = 0; nt < 4; ++nt)
         reinterpret_cast<float4*>(p)[(mt * 4 + nt) * 32 + lane] =
             make_float4(c[mt][nt][0], c[mt][nt][1], c[mt][nt][2], c[mt][nt][3]);
+  }
+  // The same in shared memory.
+  __device__ __forceinline__ void put(uint32_t at, int lane) const {
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt)
+        sts4(at + ((mt * 4 + nt) * 32 + lane) * 16, __float_as_uint(c[mt][nt][0]),
+             __float_as_uint(c[mt][nt][1]), __float_as_uint(c[mt][nt][2]),
+             __float_as_uint(c[mt][nt][3]));
+  }
+  // state = decay * state + what put() left there; a decay of zero drops it whatever it holds.
+  __device__ __forceinline__ void follow(uint32_t at, float decay, int lane) {
+    if (decay == 0.0f) zero();
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt) {
+        const uint4 v = lds4(at + ((mt * 4 + nt) * 32 + lane) * 16);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          c[mt][nt][i] = fmaf(c[mt][nt][i], decay, __uint_as_float(w[i]));
+      }
+  }
+  __device__ __forceinline__ void add_scaled(const State& o, float f) {
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[mt][nt][i] = fmaf(o.c[mt][nt][i], f, c[mt][nt][i]);
   }
   // Row-major [32][32] outside; kTransposed: this state's rows are its columns.
   template <bool kTransposed>
@@ -790,36 +852,6 @@ struct Ring {
     return cur;
   }
 };
-
-// Float `i` of shared memory at `addr`.
-__device__ __forceinline__ float lds(uint32_t addr) {
-  float x;
-  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
-  return x;
-}
-__device__ __forceinline__ uint2 lds2(uint32_t addr) {
-  uint2 x;
-  asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(addr) : "memory");
-  return x;
-}
-__device__ __forceinline__ uint4 lds4(uint32_t addr) {
-  uint4 x;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-               : "r"(addr)
-               : "memory");
-  return x;
-}
-__device__ __forceinline__ void sts(uint32_t addr, uint32_t x) {
-  asm volatile("st.shared.b32 [%0], %1;" ::"r"(addr), "r"(x) : "memory");
-}
-__device__ __forceinline__ void sts2(uint32_t addr, float x, float y) {
-  asm volatile("st.shared.v2.f32 [%0], {%1,%2};" ::"r"(addr), "f"(x), "f"(y) : "memory");
-}
-__device__ __forceinline__ void sts4(uint32_t addr, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(x), "r"(y), "r"(z), "r"(w)
-               : "memory");
-}
 
 // float32 tile -> three bf16 planes.
 template <int NB>

@@ -84,10 +84,10 @@ def test_forward_gates(cuda_device, io, gates, N):
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
-@pytest.mark.parametrize("case", [(20, 70, 130), (1, 3000, 2), (3, 1, 500), (1, 100, 1), (5, 700, 9)],
-                         ids=str)
+@pytest.mark.parametrize("case", [(20, 70, 130), (1, 3000, 2), (3, 1, 500), (1, 100, 1), (5, 700, 9), (4, 700, 55),
+                                  (6, 270, 46), (3, 1100, 90), (1, 257, 70), (1, 256, 70), (12, 129, 24)], ids=str)
 def test_forward_shapes(cuda_device, io, case):
-    """One segment per head (more heads than warps fit), many segments, odd counts."""
+    """One segment per head (more heads than warps fit), many segments, a CTA per row, odd counts."""
     _forward(case, io, "mixed", True)
 
 
@@ -175,8 +175,10 @@ def test_pieces_equal_the_whole(cuda_device, io, cuts):
     _check("S", state, S_ref, AS, _tol(io, N), HALF["f32"])
 
 
-def test_state_in_place_with_segments(cuda_device):
-    q, k, v, g, _, S, _ = _draw(1, 2000, 3, "bf16", 4)
+@pytest.mark.parametrize("case", [(1, 2000, 3), (4, 600, 60), (2, 3, 4), (1, 20, 4), (16, 50, 90)], ids=str)
+def test_state_in_place(cuda_device, case):
+    """Segments, a CTA per row, single tokens, one block, a walk per head."""
+    q, k, v, g, _, S, _ = _draw(*case, "bf16", 4)
     dev = _dev(q, k, v, g)
     state = S.cuda()
     O1, S1 = la.gated_attention(*dev, S_in=state, want_state=True)
