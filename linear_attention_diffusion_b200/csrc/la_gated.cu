@@ -924,8 +924,9 @@ cudaError_t backward(const GatedProblem& p, const void* Q, const void* K, const 
 //  - no segment so short that its start and its state cost more than its work: 64 tokens
 //    (1024 tokens of 36 heads: 10.7 us, with 32 tokens 11.8 us), 96 for much float32 work (8 x
 //    509 tokens of 36 heads: 43 us, with 64 tokens 45 us); where little is to be done at all, the
-//    time is one warp's, and 32 tokens and at most 32 segments are best (256 tokens of 36 heads:
-//    7.0 us, with 64 tokens 8.9 us).
+//    time is one warp's, and 32 tokens are best (256 tokens of 36 heads: 7.0 us, with 64 tokens
+//    8.9 us), up to a number of segments whose combination would take longer (4000 tokens of 4
+//    heads, float32 backwards: 37 us with 125 segments, 63 us with 32).
 //
 // Forwards, a CTA takes a whole row where its four warps are enough: short rows, or rows of
 // so many heads that they would not be cut much finer. In one launch against three, bf16: 256
@@ -937,11 +938,12 @@ void gated_split(GatedProblem& p, bool backward) {
   const long long BH = 1LL * p.B * p.H, work = BH * p.N;
   const bool bf16 = p.io == LA_IO_BF16;
   const long long per_sm = bf16 ? (backward ? 8 : 12) : (backward ? 6 : 10);
-  const bool little = work < (backward ? 40000 : 20000);
+  const bool little = work < (!bf16 ? 60000 : backward ? 40000 : 20000);
+  const int most = !bf16 ? 128 : backward ? 64 : 32;
   long long n = BH > 0 ? 148 * per_sm / BH : 1;
   if (n < 1) n = 1;
   if (!bf16 && n > 1) n *= 4;
-  if (little && n > 32) n = 32;
+  if (little && n > most) n = most;
   long long seg = (p.N + n - 1) / n;
   const long long least = little ? 32 : !bf16 && work >= 96000 ? 96 : 64;
   if (seg < least) seg = least;
