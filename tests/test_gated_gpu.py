@@ -175,6 +175,16 @@ def test_pieces_equal_the_whole(cuda_device, io, cuts):
     _check("S", state, S_ref, AS, _tol(io, N), HALF["f32"])
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("case", [(1, 2000, 3), (2, 1500, 40), (4, 600, 60), (1, 20, 4)], ids=str)
+def test_without_the_last_state(cuda_device, io, case):
+    q, k, v, g, _, S, _ = _draw(*case, io, 6)
+    O = la.gated_attention(*_dev(q, k, v, g), S_in=S.cuda(), scale=0.3)
+    ref, _ = orc.gated_attention(q, k, v, g, S, 0.3)
+    A, _ = orc.gated_magnitudes(q, k, v, g, S_in=S, scale=0.3)
+    _check("O", O, ref, A, _tol(io, case[1]), HALF[io])
+
+
 @pytest.mark.parametrize("case", [(1, 2000, 3), (4, 600, 60), (2, 3, 4), (1, 20, 4), (16, 50, 90)], ids=str)
 def test_state_in_place(cuda_device, case):
     """Segments, a CTA per row, single tokens, one block, a walk per head."""
