@@ -18,6 +18,11 @@
 // column sums that the parameters' gradients need, sum dy n, sum dy and sum u dh, in
 // registers; a second kernel adds the CTAs' partial sums in order. No atomics: the
 // same bits every time.
+//
+// 16384 x 2240 in bf16 with gate and modulation: forward 53 us, 5.5 TB/s (the warps' next rows
+// ahead in registers or in L2, or a CTA per row, measured slower: 58 to 71 us); backward 88 us,
+// 5.0 TB/s, of which the column sums' second kernel is 8: three sums over a row, each its shuffles
+// and a barrier, run beside the copies of the next row.
 #include "la_block_internal.h"
 #include "la_common.cuh"
 #include "la_sm100.cuh"
@@ -28,7 +33,7 @@ namespace {
 constexpr int kVec = 8;  // columns a thread moves at once
 
 // Eight numbers of an output row. Rows that are read or written once stream past L2 (loads and
-// stores marked evict-first: 59.5 instead of 62.6 us for the forward at 16384 x 2240).
+// stores marked evict-first: 3 us less for the forward at 16384 x 2240).
 __device__ __forceinline__ void store_cs(__nv_bfloat16* p, const float* x) {
   __stcs(reinterpret_cast<uint4*>(p),
          make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
