@@ -298,8 +298,8 @@ size_t la_gated_workspace_bytes(const la_gated_shape* shape, int backward);
  * itself, so a sequence can be fed in pieces of any length (prompt, then one
  * token at a time). N = 0 copies S_in to S_out. A NaN or infinity in q, k, v or
  * G may reach the outputs of all tokens of its 16-token block and of later ones (in the
- * backward also of earlier ones); a gate that lets nothing through ends that, but only
- * from the next 32 tokens on.
+ * backward, where dO counts too, also of earlier ones), but never passes a gate that lets
+ * nothing through: what is packed before and behind it stays as it is.
  * float32 sums and state; bf16 outputs are rounded once. Up to 4 tokens run as
  * one launch that walks them one by one; longer calls walk 16-token blocks on
  * the tensor cores, in one launch where the rows are short or B*H fills the GPU,

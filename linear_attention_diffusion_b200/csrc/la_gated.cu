@@ -54,6 +54,43 @@ template <bool k>
 struct Const {
   static constexpr bool value = k;
 };
+// The copies of a step's code. kStops: there may be stops, and with them something to take out;
+// kLow: sums of gates carry what their rounding left; kRagged: rows past the end are minded.
+template <bool kStops_, bool kLow_, bool kRagged_>
+struct Mode {
+  static constexpr bool kStops = kStops_, kLow = kLow_, kRagged = kRagged_;
+};
+// A step's decays: formed here for float32, and where a gate may have been taken out, else known.
+template <int NP, int NB, bool kStops, typename Known>
+__device__ __forceinline__ Decay<NP, NB> decays(const Known& known, float gate, uint32_t stops,
+                                                int lane) {
+  if constexpr (NP == 1) {
+    if (kStops && stops != 0) return Decay<NP, NB>(gate, stops, lane);
+    return known;
+  } else {
+    return Decay<NP, NB>(gate, stops, lane);
+  }
+}
+// Two copies each: bf16 one without any of the three and one with all; float32 one for steps
+// with stops and one for the others, told apart by a vote, which the compiler knows to be the
+// same for the whole warp (3 x 2003 tokens of 36 heads: 69.5 us; by the stops' bits, and with
+// their masks in the common copy too, 75 us).
+template <int NP, int NB, typename Step>
+__device__ __forceinline__ void run_step(float gate, bool ragged, int lane, const Step& step) {
+  if constexpr (NP == 1) {
+    const uint32_t stops = Decay<NP, NB>::find_stops(gate);
+    const Decay<NP, NB> d(gate, stops, lane);
+    if (d.hard || ragged)
+      step(Mode<true, true, true>(), d, stops);
+    else
+      step(Mode<false, false, false>(), d, 0u);
+  } else {
+    if (__any_sync(0xffffffffu, Decay<NP, NB>::is_stop(gate)))
+      step(Mode<true, true, true>(), 0, Decay<NP, NB>::find_stops(gate));
+    else
+      step(Mode<false, true, true>(), 0, 0u);
+  }
+}
 
 struct Walk {
   const void *q, *k, *v, *w;  // operands; w: one more tile (see each kernel)
@@ -99,7 +136,7 @@ constexpr __host__ __device__ int parts(int NP, bool precise) { return NP == 1 &
 // `acc`. kLater: the row's tokens are the later ones of each pair (forward), else the earlier
 // ones (backward). rowf: the row block's operand; colt / deept: shared-memory tiles whose
 // tokens are the columns, and the depth of the second product.
-template <int NP, int NB, int NC, bool kLater, bool kHard>
+template <int NP, int NB, int NC, bool kLater, bool kStops, bool kLow>
 __device__ __forceinline__ void block_row(float (&acc)[4][4], int b, const Frag<NP>& rowf,
                                           uint32_t colt, uint32_t deept, int plane,
                                           const LaneOff& off, const Decay<NP, NB>& d, float head,
@@ -115,7 +152,7 @@ __device__ __forceinline__ void block_row(float (&acc)[4][4], int b, const Frag<
     }
     float l[2][4];
     if (o == b) {
-      d.template within<kLater, kHard>(b, lane, l);
+      d.template within<kLater, kStops, kLow>(b, lane, l);
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -129,7 +166,7 @@ __device__ __forceinline__ void block_row(float (&acc)[4][4], int b, const Frag<
 #pragma unroll
         for (int x = 0; x < 4; ++x) l[h][x] = r[h] * c[x];
     }
-    decay_by<kHard>(w, l);
+    decay_by<kStops>(w, l);
     Frag<NP> v;
     v.deep(deept + o * kPlane, plane, off);
     if (o == b)
@@ -176,30 +213,27 @@ __device__ __forceinline__ void walk_pass(const Walk& a, const Place<kBlocks<NP>
   int n0 = at.n_begin;
   for (int it = 0; it < at.iters; ++it, n0 += kStep) {
     const uint32_t st = ring.next(lane);
-    const float gate = lds(st + NT * M::kTile + lane * 4);
-    uint32_t tile[3];
-    int plane = 0;
-    if (NP == 1) {
-#pragma unroll
-      for (int t = 0; t < 3; ++t) tile[t] = st + t * M::kTile;
-    } else {
-      plane = M::kPart;
-#pragma unroll
-      for (int t = 0; t < 3; ++t) {
-        split_tile<NB>(st + t * M::kTile, planes + t * 3 * M::kPart, lane);
-        tile[t] = planes + t * 3 * M::kPart;
-      }
-      __syncwarp();
-    }
+    float gate = lds(st + NT * M::kTile + lane * 4);
     if (kBack && (n0 - at.n_begin) % a.anchor == 0)
       S.store(anchors + static_cast<size_t>((n0 - at.n_begin) / a.anchor) * 1024, lane);
-
-    const Decay<NP, NB> d(gate, lane);
+    uint32_t tile[3];
+    const int plane = NP == 1 ? 0 : M::kPart;
+#pragma unroll
+    for (int t = 0; t < 3; ++t) tile[t] = NP == 1 ? st + t * M::kTile : planes + t * 3 * M::kPart;
     const int left = at.n_end - n0;
-    auto step = [&](auto careful) {
-      constexpr bool kHard = decltype(careful)::value;
-      const float head = d.template head<kHard>(lane), tail = d.template tail<kHard>(lane);
-      const float whole = d.template whole<kHard>(lane);
+    auto step = [&](auto mode, auto known, uint32_t stops) {
+      constexpr bool kStops = decltype(mode)::kStops, kLow = decltype(mode)::kLow;
+      uint32_t bad = 0;
+      if (kStops && stops != 0)
+        bad = take_out_gates<NB>(gate) | take_out<NP, NB>(st + M::kTile, st + 2 * M::kTile, lane);
+      if (NP > 1) {
+#pragma unroll
+        for (int t = 0; t < 3; ++t) split_tile<NB>(st + t * M::kTile, tile[t], lane);
+        __syncwarp();
+      }
+      const Decay<NP, NB> d = decays<NP, NB, kStops>(known, gate, stops, lane);
+      const float head = d.template head<kStops>(lane), tail = d.template tail<kStops, kLow>(lane);
+      const float whole = d.template whole<kStops>(lane);
       // decays of the step's blocks, from its start and to its end
       const float w0 = __shfl_sync(0xffffffffu, whole, 0);
       const float w1 = NB == 1 ? 1.0f : __shfl_sync(0xffffffffu, whole, 16);
@@ -215,10 +249,12 @@ __device__ __forceinline__ void walk_pass(const Walk& a, const Place<kBlocks<NP>
         for (int b = 0; b < NB; ++b) {
           float r[2];
           Decay<NP, NB>::spread_rows(from_start, b, lane, r);
-          scale_row<kHard>(acc[b], 0, r[0]);
-          scale_row<kHard>(acc[b], 1, r[1]);
-          block_row<NP, NB, NC, true, kHard>(acc[b], b, q[b], tile[1], tile[2], plane, off, d, head,
+          scale_row<kStops>(acc[b], 0, r[0]);
+          scale_row<kStops>(acc[b], 1, r[1]);
+          block_row<NP, NB, NC, true, kStops, kLow>(acc[b], b, q[b], tile[1], tile[2], plane, off, d, head,
                                              tail, p.scale, lane);
+          if (kStops && bad != 0)
+            spoil_rows<NP, NB>(acc[b], b, spoiled_from(bad, stops, lane & (kStep - 1)), lane);
         }
       }
       {
@@ -230,7 +266,8 @@ __device__ __forceinline__ void walk_pass(const Walk& a, const Place<kBlocks<NP>
           v[b].deep(tile[2] + b * kPlane, plane, off);
           k[b].deep(tile[1] + b * kPlane, plane, off);
         }
-        S.template update<NP, NB, kExact ? 3 : 2, kHard>(w0 * w1, v, k, wt);
+        S.template update<NP, NB, kExact ? 3 : 2, kStops>(w0 * w1, v, k, wt);
+        if (kStops && bad != 0 && spoiled_from(bad, stops, kStep - 1) != 0.0f) S.spoil();
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -246,8 +283,8 @@ __device__ __forceinline__ void walk_pass(const Walk& a, const Place<kBlocks<NP>
           }
           if ((lane & 3) == 0) {
             float* r = a.rows + static_cast<size_t>(at.bh) * p.N + n0 + b * kGateBlock + r0;
-            if (!kHard || r0 + b * kGateBlock < left) r[0] = dots[0];
-            if (!kHard || r0 + b * kGateBlock + 8 < left) r[8] = dots[1];
+            if (!decltype(mode)::kRagged || r0 + b * kGateBlock < left) r[0] = dots[0];
+            if (!decltype(mode)::kRagged || r0 + b * kGateBlock + 8 < left) r[8] = dots[1];
           }
         }
       }
@@ -255,12 +292,9 @@ __device__ __forceinline__ void walk_pass(const Walk& a, const Place<kBlocks<NP>
 #pragma unroll
       for (int b = 0; b < NB; ++b) Out<NP>::put(acc[b], st + b * M::kTile / NB, off, lane);
       __syncwarp();
-      out.template flush<kStep, !kHard>(st, left, kStep, lane);
+      out.template flush<kStep, !decltype(mode)::kRagged>(st, left, kStep, lane);
     };
-    if (d.hard || left < kStep)
-      step(Const<true>());
-    else
-      step(Const<false>());
+    run_step<NP, NB>(gate, left < kStep, lane, step);
   }
   cp_wait<0>();
   if (kBack && at.seg == p.nseg - 1)  // the state after the last token: the anchor of the row's end
@@ -344,28 +378,26 @@ walk_back_kernel(const Walk a) {
 
   for (int it = 0; it < at.iters; ++it, n0 -= kStep) {
     const uint32_t st = ring.next(lane);
-    const float gate = lds(st + NT * M::kTile + lane * 4);
+    float gate = lds(st + NT * M::kTile + lane * 4);
     const float rdot = lds(st + NT * M::kTile + 128 + lane * 4);
     uint32_t tile[NT];
-    int plane = 0;
-    if (NP == 1) {
+    const int plane = NP == 1 ? 0 : M::kPart;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) tile[t] = st + t * M::kTile;
-    } else {
-      plane = M::kPart;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        split_tile<NB>(st + t * M::kTile, planes + t * 3 * M::kPart, lane);
-        tile[t] = planes + t * 3 * M::kPart;
-      }
-      __syncwarp();
-    }
-    const Decay<NP, NB> d(gate, lane);
+    for (int t = 0; t < NT; ++t) tile[t] = NP == 1 ? st + t * M::kTile : planes + t * 3 * M::kPart;
     const int left = at.n_end - n0;
-    auto step = [&](auto careful) {
-      constexpr bool kHard = decltype(careful)::value;
-      const float head = d.template head<kHard>(lane), tail = d.template tail<kHard>(lane);
-      const float whole = d.template whole<kHard>(lane);
+    auto step = [&](auto mode, auto known, uint32_t stops) {
+      constexpr bool kStops = decltype(mode)::kStops, kLow = decltype(mode)::kLow;
+      uint32_t bad = 0;
+      if (kStops && stops != 0)
+        bad = take_out_gates<NB>(gate) | take_out<NP, NB>(st + 2 * M::kTile, st + 3 * M::kTile, lane);
+      if (NP > 1) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) split_tile<NB>(st + t * M::kTile, tile[t], lane);
+        __syncwarp();
+      }
+      const Decay<NP, NB> d = decays<NP, NB, kStops>(known, gate, stops, lane);
+      const float head = d.template head<kStops>(lane), tail = d.template tail<kStops, kLow>(lane);
+      const float whole = d.template whole<kStops>(lane);
       const float w0 = __shfl_sync(0xffffffffu, whole, 0);
       const float w1 = NB == 1 ? 1.0f : __shfl_sync(0xffffffffu, whole, 16);
       const float to_end = NB == 2 && lane < 16 ? tail * w1 : tail;
@@ -387,11 +419,13 @@ walk_back_kernel(const Walk a) {
         for (int b = 0; b < NB; ++b) {
           float r[2];
           Decay<NP, NB>::spread_rows(to_end, b, lane, r);
-          scale_row<kHard>(acc[b], 0, r[0]);
-          scale_row<kHard>(acc[b], 1, r[1]);
-          block_row<NP, NB, which == 0 ? NK : NV, false, kHard>(
+          scale_row<kStops>(acc[b], 0, r[0]);
+          scale_row<kStops>(acc[b], 1, r[1]);
+          block_row<NP, NB, which == 0 ? NK : NV, false, kStops, kLow>(
               acc[b], b, x[b], tile[3 - which], tile[2 + which], plane, off, d, head, tail, p.scale,
               lane);
+          if (kStops && bad != 0)
+            spoil_rows<NP, NB>(acc[b], b, spoiled_to(bad, stops, lane & (kStep - 1)), lane);
         }
         if (which == 0) {
 #pragma unroll
@@ -410,7 +444,7 @@ walk_back_kernel(const Walk a) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) Out<NP>::put(acc[b], pass + b * M::kTile / NB, off, lane);
         __syncwarp();
-        (which == 0 ? out_k : out_v).template flush<kStep, !kHard>(pass, left, -kStep, lane);
+        (which == 0 ? out_k : out_v).template flush<kStep, !decltype(mode)::kRagged>(pass, left, -kStep, lane);
       };
       side(Const<false>());
       side(Const<true>());
@@ -423,10 +457,11 @@ walk_back_kernel(const Walk a) {
           q[b].deep(tile[2] + b * kPlane, plane, off);
           o[b].deep(tile[3] + b * kPlane, plane, off);
         }
-        X.template update<NP, NB, 3, kHard>(w0 * w1, q, o, wt);
+        X.template update<NP, NB, 3, kStops>(w0 * w1, q, o, wt);
+        if (kStops && bad != 0 && spoils_start(bad, stops)) X.spoil();
       }
-      // dg_t = dg_{t+1} + q_t . dq_t - k_t . dk_t, summed from the step's end; a stop
-      // passes no gradient and restarts the sum
+      // dg_t = dg_{t+1} + q_t . dq_t - k_t . dk_t, summed from the step's end, or from the next
+      // stop, which passes no gradient
       const int i = lane & (kStep - 1);
       float own = 0.0f;
 #pragma unroll
@@ -437,26 +472,20 @@ walk_back_kernel(const Walk a) {
           if ((i >> 3) == 2 * b + h) own = y;
         }
       float x = rdot - own;
+      const uint32_t after = kStops ? stops & ~((2u << i) - 1u) : 0u;
+      const int end = after != 0 ? __ffs(after) - 1 : kStep;
 #pragma unroll
       for (int s = 1; s < kStep; s <<= 1) {
         const float y = __shfl_down_sync(0xffffffffu, x, s, kStep);
-        if (i + s < kStep) x += y;
+        if (i + s < end) x += y;
       }
-      float dg = carry + x;
-      if (kHard && d.stops != 0) {
-        const uint32_t after = d.stops & ~((2u << i) - 1u);
-        const float cut = __shfl_sync(0xffffffffu, x, after != 0 ? __ffs(after) - 1 : 0);
-        if (after != 0) dg = x - cut;
-        if ((d.stops >> i) & 1u) dg = 0.0f;
-      }
-      if (lane < kStep && (!kHard || i < left))
+      float dg = after != 0 ? x : carry + x;
+      if (kStops && ((stops >> i) & 1u)) dg = 0.0f;
+      if (lane < kStep && (!decltype(mode)::kRagged || i < left))
         a.dG[at.gbase + static_cast<size_t>(n0 + i) * p.H] = dg;
       carry = __shfl_sync(0xffffffffu, dg, 0);
     };
-    if (d.hard || left < kStep)
-      step(Const<true>());
-    else
-      step(Const<false>());
+    run_step<NP, NB>(gate, left < kStep, lane, step);
     if ((n0 - at.n_begin) % a.anchor == 0 && it + 1 < at.iters) {
       State S;
       S.load(anchors + static_cast<size_t>((n0 - at.n_begin) / a.anchor) * 1024, lane);
@@ -504,30 +533,32 @@ __device__ __forceinline__ void segment_pass(const GatedProblem& p, const Place<
   const LaneOff off(lane);
   for (int it = 0; it < at.iters; ++it) {
     const uint32_t st = ring.next(lane);
-    const float gate = lds(st + NT * M::kTile + lane * 4);
+    float gate = lds(st + NT * M::kTile + lane * 4);
     uint32_t tile[NT];
-    int plane = 0;
-    if (NP == 1) {
+    const int plane = NP == 1 ? 0 : M::kPart;
 #pragma unroll
-      for (int t = 0; t < NT; ++t) tile[t] = st + t * M::kTile;
-    } else {
-      plane = M::kPart;
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        split_tile<NB>(st + t * M::kTile, planes + t * 3 * M::kPart, lane);
-        tile[t] = planes + t * 3 * M::kPart;
+    for (int t = 0; t < NT; ++t) tile[t] = NP == 1 ? st + t * M::kTile : planes + t * 3 * M::kPart;
+    auto step = [&](auto mode, auto known, uint32_t stops) {
+      constexpr bool kStops = decltype(mode)::kStops, kLow = decltype(mode)::kLow;
+      uint32_t bad = 0, bad_x = 0;
+      if (kStops && stops != 0) {
+        const uint32_t gates = take_out_gates<NB>(gate);
+        bad = gates | take_out<NP, NB>(st, st + M::kTile, lane);
+        if (kBack)
+          bad_x = gates | take_out<NP, NB>(st + (NT - 2) * M::kTile, st + (NT - 1) * M::kTile, lane);
       }
-      __syncwarp();
-    }
-    const Decay<NP, NB> d(gate, lane);
-    auto step = [&](auto careful) {
-      constexpr bool kHard = decltype(careful)::value;
-      const float whole = d.template whole<kHard>(lane);
+      if (NP > 1) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t) split_tile<NB>(st + t * M::kTile, tile[t], lane);
+        __syncwarp();
+      }
+      const Decay<NP, NB> d = decays<NP, NB, kStops>(known, gate, stops, lane);
+      const float whole = d.template whole<kStops>(lane);
       const float w0 = __shfl_sync(0xffffffffu, whole, 0);
       const float w1 = NB == 1 ? 1.0f : __shfl_sync(0xffffffffu, whole, 16);
       float w[NB][4];
       if (!kBack || total != 0.0f) {
-        const float tail = d.template tail<kHard>(lane);
+        const float tail = d.template tail<kStops, kLow>(lane);
         const float to_end = (NB == 2 && lane < 16 ? tail * w1 : tail) * total;
         Frag<NP> x[NB], y[NB];
 #pragma unroll
@@ -537,9 +568,10 @@ __device__ __forceinline__ void segment_pass(const GatedProblem& p, const Place<
           y[b].deep(tile[1] + b * kPlane, plane, off);
         }
         S.template update<NP, NB, kExact ? 3 : 2, false>(1.0f, x, y, w);
+        if (kStops && bad != 0 && spoiled_from(bad, stops, kStep - 1) != 0.0f) S.spoil();
       }
       if (kBack) {
-        const float head = d.template head<kHard>(lane);
+        const float head = d.template head<kStops>(lane);
         const float from_start = (NB == 2 && lane >= 16 ? head * w0 : head) * p.scale;
         Frag<NP> x[NB], y[NB];
 #pragma unroll
@@ -548,14 +580,12 @@ __device__ __forceinline__ void segment_pass(const GatedProblem& p, const Place<
           x[b].deep(tile[NT - 2] + b * kPlane, plane, off);
           y[b].deep(tile[NT - 1] + b * kPlane, plane, off);
         }
-        X.template update<NP, NB, 3, kHard>(w0 * w1, x, y, w);
+        X.template update<NP, NB, 3, kStops>(w0 * w1, x, y, w);
+        if (kStops && bad_x != 0 && spoils_start(bad_x, stops)) X.spoil();
       }
       total *= w0 * w1;
     };
-    if (d.hard)
-      step(Const<true>());
-    else
-      step(Const<false>());
+    run_step<NP, NB>(gate, false, lane, step);
     if (!kBack && total == 0.0f) break;
   }
   cp_wait<0>();

@@ -47,6 +47,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // it is kept apart from the sums of the others, where it would cost their
 // precision (and -inf would give NaN).
 constexpr float kStop = -150.0f;
+constexpr int kNan = 0x7fffffff;
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -375,6 +376,14 @@ struct State {
           c[mt][nt][i] = fmaf(c[mt][nt][i], decay, __uint_as_float(w[i]));
       }
   }
+  __device__ __forceinline__ void spoil() {
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+      for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[mt][nt][i] = __int_as_float(kNan);
+  }
   __device__ __forceinline__ void add_scaled(const State& o, float f) {
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt)
@@ -411,11 +420,11 @@ struct State {
   // state = decay * state + sum over the tokens of NB blocks of w A^T B; A gives the rows,
   // B the columns, w[b] the weights of tokens 2 (l % 4) + {0, 1, 8, 9} of block b.
   // The weighted numbers keep 24 bits (kParts = 3) or 17 (2).
-  template <int NP, int NB, int kParts, bool kHard>
+  template <int NP, int NB, int kParts, bool kStops>
   __device__ __forceinline__ void update(float decay, const Frag<NP> (&A)[NB],
                                          const Frag<NP> (&B)[NB], const float (&w)[NB][4]) {
     constexpr int NC = NP == 1 && kParts == 3 ? 4 : kParts == 2 && NP == 1 ? 2 : 3;
-    if (kHard && decay == 0.0f) zero();  // a stop drops the state whatever it holds
+    if (kStops && decay == 0.0f) zero();  // a stop drops the state whatever it holds
     uint32_t wp[NB][2][kParts];
     if (NP == 1) {
 #pragma unroll
@@ -585,25 +594,26 @@ struct State {
   }
 };
 
-// Scale one row of an accumulator; kHard: a factor of zero drops it whatever it holds.
-template <bool kHard>
+// Scale one row of an accumulator; kStops: a factor of zero drops it whatever it holds.
+template <bool kStops>
 __device__ __forceinline__ void scale_row(float (&acc)[4][4], int h, float f) {
 #pragma unroll
   for (int e = 0; e < 4; ++e)
 #pragma unroll
     for (int i = 2 * h; i < 2 * h + 2; ++i)
-      acc[e][i] = kHard && f == 0.0f ? 0.0f : acc[e][i] * f;
+      acc[e][i] = kStops && f == 0.0f ? 0.0f : acc[e][i] * f;
 }
 
 // The decays of NB blocks of 16 tokens. Lane l stands for token l % (16 NB); c is the sum of
 // log2 gates from its block's first token to it, stops left out.
 //
-// A decay is the difference of two such sums. Where a sum passes kEasy in size (and always for
+// A decay is the difference of two such sums. Where a sum falls below kEasy (and always for
 // float32 tensors) the sums carry what their rounding left in `low`, so that gates of -100 do
-// not cost the small gates next to them their low bits; below it the difference is good to
-// 2^-18. There, and where something stops, a step is `hard`: it runs a second copy of the
-// step's code that minds both, so that the ordinary one stays free of branches, one long
-// stretch in which the scheduler can lay products beside the arithmetic around them.
+// not cost the small gates next to them their low bits; above it the difference is good to
+// 2^-18 (sums of gates that let the state grow, to 2^-24 of their size). Where a bf16 step is
+// `hard`, for that or for a stop, it runs a second copy of the step's code that minds both, so
+// that the ordinary one stays free of branches, one long stretch in which the scheduler can lay
+// products beside the arithmetic around them.
 template <int NP, int NB>
 struct Decay {
   static constexpr float kEasy = NP == 1 ? -32.0f : 1.0f;
@@ -611,12 +621,14 @@ struct Decay {
   float last, last_low;  // the same at the last token of its block
   uint32_t stops;        // bit i: token i's gate lets nothing through
   bool hard;
-  __device__ __forceinline__ Decay(float g, int lane) {
+  static __device__ __forceinline__ bool is_stop(float g) { return g * kLog2e < kStop; }
+  static __device__ __forceinline__ uint32_t find_stops(float g) {
+    const uint32_t found = __ballot_sync(0xffffffffu, is_stop(g));
+    return NB == 1 ? found & 0xffffu : found;
+  }
+  __device__ __forceinline__ Decay(float g, uint32_t found, int lane) : stops(found) {
     float x = g * kLog2e;
-    const bool stop = x < kStop;
-    stops = __ballot_sync(0xffffffffu, stop);
-    if (NB == 1) stops &= 0xffffu;
-    if (stop) x = 0.0f;
+    if (x < kStop) x = 0.0f;
     const float x0 = x;
     low = last_low = 0.0f;
 #pragma unroll
@@ -649,21 +661,21 @@ struct Decay {
     return NB == 1 ? stops : (stops >> (lane & 16)) & 0xffffu;
   }
   // from the state before the lane's block to its token
-  template <bool kHard>
+  template <bool kStops>
   __device__ __forceinline__ float head(int lane) const {
     const float f = exp2_fast(c);
-    return kHard && (own_stops(lane) & ((2u << (lane & 15)) - 1u)) ? 0.0f : f;
+    return kStops && (own_stops(lane) & ((2u << (lane & 15)) - 1u)) ? 0.0f : f;
   }
   // from the lane's token to its block's end
-  template <bool kHard>
+  template <bool kStops, bool kLow>
   __device__ __forceinline__ float tail(int lane) const {
-    const float f = exp2_fast(kHard ? (last - c) + (last_low - low) : last - c);
-    return kHard && (own_stops(lane) >> ((lane & 15) + 1)) ? 0.0f : f;
+    const float f = exp2_fast(kLow ? (last - c) + (last_low - low) : last - c);
+    return kStops && (own_stops(lane) >> ((lane & 15) + 1)) ? 0.0f : f;
   }
   // over the whole of the lane's block
-  template <bool kHard>
+  template <bool kStops>
   __device__ __forceinline__ float whole(int lane) const {
-    return kHard && own_stops(lane) ? 0.0f : exp2_fast(last);
+    return kStops && own_stops(lane) ? 0.0f : exp2_fast(last);
   }
   // of `x`, one value per token: the values of tokens 16 b + 2 (l % 4) + {0, 1, 8, 9}
   static __device__ __forceinline__ void spread(float x, int b, int lane, float (&out)[4]) {
@@ -683,12 +695,12 @@ struct Decay {
   // the two, rows the later ones (kRowsLater) or the earlier ones. Pairs in the other order,
   // or with a stop between them (the later token's own included), give 0. Of the four quarters
   // one is all zeros: columns 8-15 of rows 0-7, or rows 8-15 of columns 0-7.
-  template <bool kRowsLater, bool kHard>
+  template <bool kRowsLater, bool kStops, bool kLow>
   __device__ __forceinline__ void within(int b, int lane, float (&l)[2][4]) const {
     float cc[4], cr[2], cl[4] = {0.0f, 0.0f, 0.0f, 0.0f}, lr[2] = {0.0f, 0.0f};
     spread(c, b, lane, cc);
     spread_rows(c, b, lane, cr);
-    if (kHard) {
+    if (kLow) {
       spread(low, b, lane, cl);
       spread_rows(low, b, lane, lr);
     }
@@ -697,7 +709,7 @@ struct Decay {
     for (int h = 0; h < 2; ++h) {
       const int row = (lane >> 2) + 8 * h;
       int first = 0, end = 0;  // the column tokens that count
-      if (kHard) {
+      if (kStops) {
         if (kRowsLater) {
           const uint32_t before = st & ((2u << row) - 1u);
           first = before != 0 ? 31 - __clz(before) : 0;
@@ -717,8 +729,8 @@ struct Decay {
           continue;
         }
         float d = kRowsLater ? cr[h] - cc[x] : cc[x] - cr[h];
-        if (kHard) {
-          d += kRowsLater ? lr[h] - cl[x] : cl[x] - lr[h];
+        if (kLow) d += kRowsLater ? lr[h] - cl[x] : cl[x] - lr[h];
+        if (kStops) {
           l[h][x] = col >= first && col < end ? exp2_fast(d) : 0.0f;
         } else {
           const float f = exp2_fast(d);
@@ -729,15 +741,15 @@ struct Decay {
   }
 };
 
-// w *= l; kHard: a factor of zero drops the number whatever it is.
-template <bool kHard>
+// w *= l; kStops: a factor of zero drops the number whatever it is.
+template <bool kStops>
 __device__ __forceinline__ void decay_by(float (&w)[2][4], const float (&l)[2][4]) {
 #pragma unroll
   for (int h = 0; h < 2; ++h)
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       float& e = w[x >> 1][2 * h + (x & 1)];
-      e = kHard && l[h][x] == 0.0f ? 0.0f : e * l[h][x];
+      e = kStops && l[h][x] == 0.0f ? 0.0f : e * l[h][x];
     }
 }
 
@@ -870,6 +882,79 @@ __device__ __forceinline__ void split_tile(uint32_t src, uint32_t planes, int la
     for (int p = 0; p < 3; ++p)
       sts4(planes + p * NB * kPlane + tile_off(row, c), w[0][p], w[1][p], w[2][p], w[3][p]);
   }
+}
+
+// What is not finite and a stop in one step. A product adds up all tokens of its step, those
+// behind a stop with a weight of zero, and zero times infinity is NaN. So a step with stops takes
+// such tokens out: a gate that is no number becomes 0, a token's rows of two tiles zero. Both
+// return the tokens' bits. What they should have spoiled, the outputs and states that no stop
+// parts from them, is then set to NaN.
+template <int NB>
+__device__ __forceinline__ uint32_t take_out_gates(float& gate) {
+  const bool odd = !(gate < __int_as_float(0x7f800000));
+  const uint32_t found = __ballot_sync(0xffffffffu, odd);
+  if (odd) gate = 0.0f;
+  return NB == 1 ? found & 0xffffu : found;
+}
+// float32: also numbers so large that their first bf16 part is infinite.
+template <int NP, int NB>
+__device__ __forceinline__ uint32_t take_out(uint32_t t0, uint32_t t1, int lane) {
+  const int token = lane & (NB * kGateBlock - 1);
+  const uint32_t tile[2] = {t0, t1};
+  uint32_t at[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c)
+    at[c] = NP == 1 ? tile_off(token, c) : tile_off_f32(token, c + (lane >> 4) * 4);
+  bool bad = false;
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint4 v = lds4(tile[t] + at[c]);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        bad |= NP == 1 ? (w[i] & 0x7f80u) == 0x7f80u || (w[i] & 0x7f800000u) == 0x7f800000u
+                       : (w[i] & 0x7fffffffu) >= 0x7f7f8000u;
+    }
+  uint32_t rows = __ballot_sync(0xffffffffu, bad);
+  if (NB == 1) rows = (rows | rows >> 16) & 0xffffu;  // two lanes a token
+  if (rows != 0) {
+    if ((rows >> token) & 1u) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sts4(tile[t] + at[c], 0u, 0u, 0u, 0u);
+    }
+    __syncwarp();
+  }
+  return rows;
+}
+// Whether one of the `bad` tokens reaches token i of the step forwards: from the last stop up to i on.
+__device__ __forceinline__ float spoiled_from(uint32_t bad, uint32_t stops, int i) {
+  const uint32_t upto = (2u << i) - 1u, before = stops & upto;
+  const uint32_t from = before != 0 ? ~0u << (31 - __clz(before)) : ~0u;
+  return (bad & upto & from) != 0 ? __int_as_float(kNan) : 0.0f;
+}
+// The same backwards: from i on, up to the next stop.
+__device__ __forceinline__ float spoiled_to(uint32_t bad, uint32_t stops, int i) {
+  const uint32_t later = ~((2u << i) - 1u), after = stops & later;
+  const uint32_t upto = after != 0 ? (1u << (__ffs(after) - 1)) - 1u : ~0u;
+  return (bad & (later | (1u << i)) & upto) != 0 ? __int_as_float(kNan) : 0.0f;
+}
+// And the state before the step.
+__device__ __forceinline__ bool spoils_start(uint32_t bad, uint32_t stops) {
+  return (bad & ((stops & (0u - stops)) - 1u)) != 0;
+}
+// Add 0 or NaN to the rows of block b, by a value per token.
+template <int NP, int NB>
+__device__ __forceinline__ void spoil_rows(float (&acc)[4][4], int b, float by_token, int lane) {
+  float r[2];
+  Decay<NP, NB>::spread_rows(by_token, b, lane, r);
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[e][i] += r[i >> 1];
 }
 
 // Rows of an output: an accumulator goes to a free tile in shared memory (put), and from there

@@ -321,3 +321,40 @@ def test_a_stop_ends_what_is_not_finite(cuda_device, io, N, bad, stop):
     ref, _ = orc.gated_attention(*(x[:, :first] for x in (q, k, v, g)))
     A, _ = orc.gated_magnitudes(*(x[:, :first] for x in (q, k, v, g)))
     _check("O before", O[:, :first], ref, A, _tol(io, N), HALF[io])
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("N,bad,stop", [(3000, 705, 710), (200, 33, 36), (100, 70, 72), (24, 17, 18), (3000, 710, 705),
+                                        (200, 36, 33), (100, 72, 72), (24, 9, 3)])
+def test_a_stop_holds_inside_a_step(cuda_device, io, N, bad, stop):
+    """What is not finite (k, v or a gate, one head each) and a stop within 16 tokens of each
+    other: neither it nor what it spoils passes the stop, forwards or backwards, in the
+    outputs, the states or the gradients. Long rows in segments, a CTA per row, one walk."""
+    q, k, v, g, do, S0, dS = _draw(1, N, 4, io, 19)
+    clean = [x.clone() for x in (q, k, v, g, do)]
+    g[:, stop] = clean[3][:, stop] = -float("inf")
+    if bad != stop:
+        g[:, bad, 0] = float("nan")
+    v[:, bad, 1] = float("nan")
+    k[:, bad, 2] = float("inf")
+    do[:, bad, 3] = float("nan")
+    tol = _tol(io, N)
+    after = bad < stop
+    part = slice(stop, N) if after else slice(0, stop)
+    cut = [x[:, part] for x in clean]
+    first, last = (None, dS) if after else (S0, None)
+    ref, S_ref = orc.gated_attention(*cut[:4], first)
+    A, AS = orc.gated_magnitudes(*cut[:4], S_in=first)
+    dev = _dev(q, k, v, g)
+    O, S = la.gated_attention(*dev, S_in=S0.cuda(), want_state=True)
+    _check("O", O[:, part], ref, A, tol, HALF[io])
+    _check("O alone", la.gated_attention(*dev, S_in=S0.cuda())[:, part], ref, A, tol, HALF[io])
+    if after:
+        _check("S", S, S_ref, AS, tol, HALF["f32"])
+    grads = la.gated_attention_backward(*dev, do.cuda(), S_in=S0.cuda(), dS_out=dS.cuda())
+    refs = orc.gated_attention_backward(*cut, first, last)
+    mags = orc.gated_magnitudes(*cut, first, last)
+    for i, name in enumerate(("dQ", "dK", "dV", "dG")):
+        _check(name, grads[i][:, part], refs[i], mags[i], 2 * tol, HALF[io] if i < 3 else HALF["f32"])
+    if not after:
+        _check("dS_in", grads[4], refs[4], mags[4], tol, HALF["f32"])
