@@ -36,6 +36,7 @@ from .gated import (  # noqa: F401,E402
     gated_attention_backward,
     gated_bruteforce,
     gated_magnitudes,
+    gated_window_errors,
 )
 from .rotary import rotary, rotary_rates  # noqa: F401,E402
 from .norm import gate_residual_norm, gate_residual_norm_backward  # noqa: F401,E402

@@ -93,3 +93,15 @@ def gated_magnitudes(Q, K, V, G, dO=None, S_in=None, dS_out=None, scale: float =
         last = (dS * SN).sum((-1, -2))[:, None]
     at_end = dG.max(1, keepdims=True)
     return dQ, dK, dV, dG + (total[:, end] - total[:, :N]) + at_end + last, dS0
+
+
+def gated_window_errors(dG, ref, window: int = 256) -> np.ndarray:
+    """Relative 2-norm error of dG [B, N, H] in every head's windows of ``window`` tokens,
+    [B, windows, H]. A last window shorter than 32 tokens counts with the one before."""
+    got, ref = _f64(dG), _f64(ref)
+    N = ref.shape[1]
+    starts = list(range(0, N, window))
+    if len(starts) > 1 and N - starts[-1] < 32:
+        starts.pop()
+    sums = [np.add.reduceat(x * x, starts, axis=1) for x in (got - ref, ref)]
+    return np.sqrt(sums[0] / np.maximum(sums[1], 1e-300))

@@ -156,3 +156,25 @@ def test_binding_refuses_what_does_not_fit():
         la.gated_attention_backward(q, q, q, g, t(1, 5, 2, 32, dt=f))
     with pytest.raises(ValueError):
         la.gated_attention_backward(q, q, q, g, q, dS_out=t(1, 2, 32, 32))
+
+
+def test_window_errors_see_what_a_gate_gradient_can_lose():
+    """The bound of the GPU's check (2^-15) is far below what zeros, a lost carry between two
+    windows of 256 tokens, or a stale one give; the oracle's own numbers in float32 stay below."""
+    r = np.random.default_rng(5)
+    B, N, H, D = 1, 600, 3, 8
+    q, k, v, do = (r.standard_normal((B, N, H, D)) for _ in range(4))
+    g = -r.uniform(0.002, 0.5, H) * r.uniform(0.1, 2.1, (B, N, H))
+    S, dS = r.standard_normal((2, B, H, D, D))
+    dQ, dK, _, dG, _ = orc.gated_attention_backward(q, k, v, g, do, S, dS, 0.4)
+    err = lambda x: orc.gated_window_errors(x, dG)  # noqa: E731
+    assert err(dG.astype(np.float32)).max() < 2.0 ** -23
+    assert (err(np.zeros_like(dG)) == 1.0).all() and err(dG).shape == (1, 3, 3)
+    rows = (q * dQ).sum(-1) - (k * dK).sum(-1)
+    for lost, at in ((dG[:, 256], slice(0, 256)), (dG[:, 512], slice(256, 512))):
+        x = dG.copy()
+        x[:, at] -= lost[:, None]                     # the sum of the window's rows alone
+        assert np.allclose(x[:, at], rows[:, at][:, ::-1].cumsum(1)[:, ::-1], atol=1e-9)
+        assert (err(x).max(1) > 2.0 ** -4).all()
+        x[:, at] += dG[:, 100][:, None]               # another place's carry
+        assert (err(x).max(1) > 2.0 ** -4).all()

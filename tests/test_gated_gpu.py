@@ -358,3 +358,24 @@ def test_a_stop_holds_inside_a_step(cuda_device, io, N, bad, stop):
         _check(name, grads[i][:, part], refs[i], mags[i], 2 * tol, HALF[io] if i < 3 else HALF["f32"])
     if not after:
         _check("dS_in", grads[4], refs[4], mags[4], tol, HALF["f32"])
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("gates", ["mixed", "packed"])
+@pytest.mark.parametrize("B,N,H", [(1, 3000, 6), (1, 600, 920), (2, 700, 5)], ids=str)
+def test_gate_gradients_window_by_window(cuda_device, io, gates, B, N, H):
+    """dG in the 2-norm of every head's windows of 256 tokens: the sums between two anchors, their
+    carry from one segment to the next, stops between them. B H = 920 rows are not cut, so a
+    segment holds two inner anchors. Bound 2^-15: a row product carries 2^-19 of its terms (two
+    chains of some 16 float32 sums), and the up to 256 of them in a gate's gradient add up like
+    independent errors, 2^4 of that; gradient and row products are of one size in this draw.
+    All zeros, or a window whose carry is lost, are off by more than 2^-4 (test_gated_cpu.py)."""
+    q, k, v, g, do, S, dS = _draw(B, N, H, io, 23)
+    if gates == "packed":
+        g[torch.rand((B, N), generator=torch.Generator().manual_seed(2)) < 0.01] = -float("inf")
+    dG = la.gated_attention_backward(*_dev(q, k, v, g, do), S_in=S.cuda(), dS_out=dS.cuda(), scale=0.4)[3]
+    some = [0, H // 2, H - 1]  # heads are independent
+    cut = [x[:, :, some] for x in (q, k, v, g, do)] + [x[:, some] for x in (S, dS)]
+    ref = orc.gated_attention_backward(*cut, 0.4)[3]
+    err = orc.gated_window_errors(dG[:, :, some].cpu(), ref)
+    assert err.max() <= 2.0 ** -15, err.max()
