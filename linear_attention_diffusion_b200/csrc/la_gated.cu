@@ -818,20 +818,28 @@ step_kernel(const GatedProblem p, const T* Q, const T* K, const T* V, const floa
   }
 }
 
+// Shared memory of a launch, and the most that any call of the kernel takes: its limit is set to
+// that, never to the call's own, which another thread's call could undo before the launch.
+struct SmemBytes {
+  int bytes, most;
+  SmemBytes(int fixed) : bytes(fixed), most(fixed) {}
+  SmemBytes(int b, int m) : bytes(b), most(m) {}
+};
+
 // Launch a kernel with its shared memory. chained: it may start while the kernel before it on
 // the stream, one of this call's own, still runs, and waits for it itself (pdl_wait).
 template <typename... Params, typename... Args>
-cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, int smem, bool chained,
+cudaError_t launch(void (*kernel)(Params...), dim3 grid, int threads, SmemBytes smem, bool chained,
                    cudaStream_t s, Args... args) {
-  if (smem > 48 * 1024) {
+  if (smem.most > 48 * 1024) {
     const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem.most);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem.bytes);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -864,7 +872,7 @@ cudaError_t forward(const GatedProblem& p, const void* Q, const void* K, const v
   if (p.whole_row) {
     a.final_ = S_out;
     return launch(row_kernel<NP>, dim3(static_cast<unsigned>(BH)), p.nseg * 32,
-                  p.nseg * RowSmem<NP>::kWarp, false, s, a);
+                  {p.nseg * RowSmem<NP>::kWarp, kRowWarps * RowSmem<NP>::kWarp}, false, s, a);
   }
   float* states = ws;
   if (p.nseg > 1) {

@@ -557,11 +557,18 @@ norm_columns_kernel(const NormProblem p, const NormParams w, const NormGrads g, 
   }
 }
 
+// `most`: what the widest row of the kernel takes, not the call's own bytes, which another
+// thread's call could undo before the launch.
 template <typename Kernel>
-cudaError_t allow_smem(Kernel k, size_t bytes) {
-  if (bytes <= 48 * 1024) return cudaSuccess;
+cudaError_t allow_smem(Kernel k, size_t most) {
+  if (most <= 48 * 1024) return cudaSuccess;
   return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(bytes));
+                              static_cast<int>(most));
+}
+constexpr size_t forward_smem(size_t C) { return (3 * C + kScratch) * sizeof(float); }
+template <typename T>
+constexpr size_t backward_smem(size_t C, size_t threads) {
+  return (2 * C + kScratch) * sizeof(float) + 4 * threads * kBackVecs * kVec * sizeof(T);
 }
 
 constexpr long long kSms = 148;
@@ -569,9 +576,9 @@ constexpr long long kSms = 148;
 template <typename T, int KV, bool kOneWarp>
 cudaError_t run_forward(const NormProblem& p, int threads, const void* x, const void* f,
                         const NormParams& w, void* h, void* y, cudaStream_t s) {
-  const size_t smem = (3 * static_cast<size_t>(p.C) + kScratch) * sizeof(float);
+  const size_t smem = forward_smem(p.C);
   auto kernel = norm_kernel<T, KV, kOneWarp>;
-  cudaError_t e = allow_smem(kernel, smem);
+  cudaError_t e = allow_smem(kernel, forward_smem(kOneWarp ? KV * kVec * 32 : kNormMaxC));
   if (e != cudaSuccess) return e;
   int resident = 0;  // a CTA for every place on the GPU: each then walks its rows
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&resident, kernel, threads, smem);
@@ -614,12 +621,11 @@ cudaError_t run_backward(const NormProblem& p, const void* x, const void* f, con
                          const void* dh, const void* dy, void* dx, void* df, float* ws,
                          cudaStream_t s) {
   const int threads = backward_threads(p.C);
-  const size_t smem = (2 * static_cast<size_t>(p.C) + kScratch) * sizeof(float) +
-                      4 * static_cast<size_t>(threads) * kBackVecs * kVec * sizeof(T);
+  const size_t smem = backward_smem<T>(p.C, threads);
   auto kernel = f != nullptr && dh != nullptr && dy != nullptr
                     ? norm_backward_kernel<T, kThreads, true>
                     : norm_backward_kernel<T, kThreads, false>;
-  const cudaError_t e = allow_smem(kernel, smem);
+  const cudaError_t e = allow_smem(kernel, backward_smem<T>(kThreads * kBackVecs * kVec, kThreads));
   if (e != cudaSuccess) return e;
   kernel<<<dim3(static_cast<unsigned>(p.ctas), static_cast<unsigned>(p.B)), threads, smem, s>>>(
       p, static_cast<const T*>(x), static_cast<const T*>(f), w,

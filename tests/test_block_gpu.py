@@ -124,3 +124,64 @@ def test_block_gradients_equal_differences(cuda_device):
         # 1e-4 of the sum's size: float32 chains of five operators (2^-20 each) and a central
         # difference with a step of 1e-5 in float64 (1e-9 of the loss / step)
         assert abs((got * way).sum() - slope) <= 1e-4 * np.linalg.norm(got * way) + 1e-4 * abs(slope), name
+
+
+def test_threads_with_different_sizes(cuda_device):
+    """Calls of the same kernels at sizes that need different shared memory, from four threads on
+    four streams, as fast as the C functions take them: none is refused, and the numbers are the
+    ones that a call gives alone."""
+    import ctypes
+    import threading
+    dev = torch.device("cuda:0")
+    gen = torch.Generator(device=dev).manual_seed(11)
+    randn = lambda *s: torch.randn(s, generator=gen, device=dev)  # noqa: E731
+    at = lambda *ts: [None if t is None else t.data_ptr() for t in ts]  # noqa: E731
+
+    def gated(N):  # float32 rows of 64 and 128 tokens: two and four warps of one kernel
+        q, k, v = (randn(2, N, 4, D) for _ in range(3))
+        g, out = -torch.rand((2, N, 4), generator=gen, device=dev), torch.empty_like(q)
+        shape = la.make_gated_shape(2, N, 4, io_dtype="f32")
+        assert la.la_gated_workspace_bytes(shape) == 256  # one launch without segments
+        args = [ctypes.byref(shape), *at(q, k, v, g, None, None, out, None), 0]
+        return (q, k, v, g, shape), out, lambda st: la._lib.la_gated_attention(*args, st)
+
+    def norm(width):
+        x, f, h, y = (randn(1, 4, width) for _ in range(4))
+        shape = la.make_norm_shape(1, 4, width, "f32")
+        args = [ctypes.byref(shape), *at(x, f, None, None, None, None, None, h, y)]
+        return (x, f, h, shape), y, lambda st: la._lib.la_gate_residual_norm(*args, st)
+
+    def norm_back(width):
+        x, f, dh, dy, dx, df = (randn(1, 4, width) for _ in range(6))
+        shape = la.make_norm_shape(1, 4, width, "f32")
+        n = la.la_norm_workspace_bytes(shape)
+        ws = torch.empty(n, dtype=torch.uint8, device=dev)
+        args = [ctypes.byref(shape), *at(x, f, None, None, None, None, dh, dy, dx, df, *[None] * 5, ws), n]
+        return (x, f, dh, dy, df, ws, shape), dx, lambda st: la._lib.la_gate_residual_norm_backward(*args, st)
+
+    for make, sizes in ((gated, (64, 128)), (norm, (4608, 8192)), (norm_back, (1408, 2560)), (norm_back, (2816, 8192))):
+        calls = [make(sizes[i % 2]) for i in range(4)]
+        want = []
+        for _, out, call in calls:
+            assert call(torch.cuda.current_stream().cuda_stream) == la.LA_OK
+            want.append(out.clone())
+        torch.cuda.synchronize()
+        refused, wrong, start = [0] * 4, [0] * 4, threading.Barrier(4)
+
+        def work(i):
+            _, out, call = calls[i]
+            stream = torch.cuda.Stream(dev)
+            raw = stream.cuda_stream
+            start.wait()
+            for _ in range(60):
+                for _ in range(200):
+                    refused[i] += call(raw) != la.LA_OK
+                stream.synchronize()
+                wrong[i] += not torch.equal(out, want[i])
+
+        threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert refused == [0] * 4 and wrong == [0] * 4, (make.__name__, sizes, refused, wrong)
