@@ -1097,7 +1097,8 @@ def main():
     peak, peak_src = peaks()
     lb = layer_bytes(w)
     lb["temporal_conv"] = 2 * r["per_set_bytes"] + r.get("cache_bytes", 0)
-    lb[args.op] = r.get("op_bytes", 0)
+    if args.op in BLOCK_OPS:
+        lb[args.op] = r["op_bytes"]
     # The unit timed is one library call: its average duration is the timed
     # region (back-to-back graph replays, no events between launches) divided
     # by the calls in it. The event graph's per-call figure, which also holds
