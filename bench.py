@@ -676,7 +676,7 @@ def run_block_op(args, w, rank, world, local_rank):
                                                ws, st)
             else:
                 la.la_gated_attention(shape, *ins, G, None, None, o[0], ws, st)
-        launches = (4 if back else 3) if ws.numel() > 256 else 1
+        launches = la.la_gated_launches(shape, back)
     elif args.op == "rotary":
         shape = la.make_rotary_shape(B, N, H, H, D)
         launches = 1

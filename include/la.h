@@ -287,6 +287,11 @@ typedef struct {
  * Pure host function. */
 size_t la_gated_workspace_bytes(const la_gated_shape* shape, int backward);
 
+/* Kernel launches of a call of la_gated_attention (backward = 0) or
+ * la_gated_attention_backward (1): 0 without tokens or for an invalid shape. Pure
+ * host function. */
+int la_gated_launches(const la_gated_shape* shape, int backward);
+
 /* Gated linear attention: token-causal, with a decay per token and head,
  *   S_n = exp(g_n) S_{n-1} + k_n^T v_n,   o_n = scale q_n S_n,   S_{-1} = S_in.
  * Without feature map or normaliser: apply a feature map to q and k before, a

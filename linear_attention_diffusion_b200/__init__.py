@@ -118,6 +118,8 @@ _lib.la_qkv_state.restype = _i
 _gated_p = ctypes.POINTER(LaGatedShape)
 _lib.la_gated_workspace_bytes.argtypes = [_gated_p, _i]
 _lib.la_gated_workspace_bytes.restype = _sz
+_lib.la_gated_launches.argtypes = [_gated_p, _i]
+_lib.la_gated_launches.restype = _i
 _lib.la_gated_attention.argtypes = [_gated_p] + [_vp] * 8 + [_sz, _vp]
 _lib.la_gated_attention.restype = _i
 _lib.la_gated_attention_backward.argtypes = [_gated_p] + [_vp] * 13 + [_sz, _vp]
@@ -270,6 +272,11 @@ def make_gated_shape(B: int, N: int, H: int, D: int = HEAD_DIM, io_dtype: str = 
 
 def la_gated_workspace_bytes(shape: LaGatedShape, backward: bool = False) -> int:
     return int(_lib.la_gated_workspace_bytes(ctypes.byref(shape), int(bool(backward))))
+
+
+def la_gated_launches(shape: LaGatedShape, backward: bool = False) -> int:
+    """Kernel launches of a call; 0 without tokens or for an invalid shape."""
+    return int(_lib.la_gated_launches(ctypes.byref(shape), int(bool(backward))))
 
 
 def la_gated_attention(shape: LaGatedShape, Q, K, V, G, S_in, S_out, O, ws, stream=None) -> None:

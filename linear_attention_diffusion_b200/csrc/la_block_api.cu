@@ -114,6 +114,15 @@ size_t la_gated_workspace_bytes(const la_gated_shape* shape, int backward) {
   return n == 0 ? 256 : n;
 }
 
+int la_gated_launches(const la_gated_shape* shape, int backward) {
+  GatedProblem p;
+  if (make_gated(shape, backward != 0, p) != LA_OK) return 0;
+  if (p.B == 0 || p.H == 0 || p.N == 0) return 0;
+  const bool cut = p.nseg > 1 && !p.whole_row;  // segments' states and their combination first
+  if (backward) return cut ? 4 : 2;
+  return cut && p.N > kGateStepTokens ? 3 : 1;
+}
+
 la_status la_gated_attention(const la_gated_shape* shape, const void* Q, const void* K,
                              const void* V, const float* G, const float* S_in, float* S_out,
                              void* O, void* ws, size_t ws_bytes, la_stream stream) {

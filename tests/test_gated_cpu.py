@@ -178,3 +178,14 @@ def test_window_errors_see_what_a_gate_gradient_can_lose():
         assert (err(x).max(1) > 2.0 ** -4).all()
         x[:, at] += dG[:, 100][:, None]               # another place's carry
         assert (err(x).max(1) > 2.0 ** -4).all()
+
+
+def test_launches_follow_the_cut():
+    """One launch for few tokens, a row a CTA or heads that fill the GPU, three where rows are cut;
+    backwards two or four."""
+    f, b = (lambda *a: la.la_gated_launches(la.make_gated_shape(*a), False),
+            lambda *a: la.la_gated_launches(la.make_gated_shape(*a), True))
+    assert f(64, 1, 70) == 1 and f(1, 256, 70) == 1 and f(64, 4096, 70) == 1 and f(1, 32760, 70) == 3
+    assert b(1, 16384, 70) == 4 and b(64, 4096, 70) == 2 and b(1, 3, 2) == 2
+    assert f(2, 0, 3) == 0 and b(0, 9, 3) == 0 and f(1, 4, 2, 64) == 0 and b(-1, 4, 2) == 0
+
