@@ -70,6 +70,15 @@ __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
   return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
                     __float_as_uint(x[3]));
 }
+// The first `pairs` pairs of `turned`, the others as they were: a NaN would lose its bits on the
+// way through float32. A float32 piece is no conversion.
+__device__ __forceinline__ uint4 keep_bits(const uint4& turned, const uint4& was, int pairs, const float (&)[8]) {
+  return make_uint4(turned.x, pairs > 1 ? turned.y : was.y, pairs > 2 ? turned.z : was.z,
+                    pairs > 3 ? turned.w : was.w);
+}
+__device__ __forceinline__ uint4 keep_bits(const uint4& turned, const uint4&, int, const float (&)[4]) {
+  return turned;
+}
 __device__ __forceinline__ void turn(float a, float b, float2 cs, float& x, float& y) {
   x = fmaf(a, cs.x, -b * cs.y);
   y = fmaf(a, cs.y, b * cs.x);
@@ -170,7 +179,7 @@ rotary_kernel(const RotaryProblem p, int tokens, const Divide share, const Divid
               const float a = x[2 * j], b = x[2 * j + 1];
               turn(a, b, cs[j0 + j], x[2 * j], x[2 * j + 1]);
             }
-          u[f] = pack(x);
+          u[f] = keep_bits(pack(x), u[f], pairs - j0, x);
         }
         __stcs(reinterpret_cast<uint4*>(dst[f] + item[f] * V), u[f]);
       } else if (kLayout == kHalves) {

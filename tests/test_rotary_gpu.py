@@ -129,3 +129,15 @@ def test_in_a_graph_and_on_another_stream(cuda_device):
     torch.cuda.synchronize()
     want = la.rotary(q, k, positions=pos)
     assert all(torch.equal(a, b) for a, b in zip(held, want))
+
+
+@pytest.mark.parametrize("layout,rot", [("interleaved", 22), ("interleaved", 2), ("interleaved", 24), ("half", 22),
+                                        ("half", 16)])
+def test_passed_dimensions_keep_their_bits(cuda_device, layout, rot):
+    """Every 16-bit pattern, the many NaNs among them, in the dimensions that pass; `rot` = 22 and
+    2 end inside a 16-byte piece."""
+    bits = torch.arange(-2 ** 15, 2 ** 15, dtype=torch.int32).to(torch.int16)
+    x = bits.reshape(1, -1, 1, 1).expand(1, -1, 2, 32).contiguous().view(torch.bfloat16).cuda()
+    x[..., :rot] = 1.0
+    y, _ = la.rotary(x, rot=rot, layout=layout)
+    assert torch.equal(y.view(torch.int16)[..., rot:], x.view(torch.int16)[..., rot:])
