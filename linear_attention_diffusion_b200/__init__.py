@@ -264,9 +264,16 @@ def la_qkv_state(shape: LaShape, C: int, X, W, bias, Q, S, z, ws, stream=None) -
            "la_qkv_state")
 
 
+def _fit(*sizes: int) -> None:
+    """Raise ValueError for a number that a C int would cut to its low 32 bits."""
+    if max(sizes) > 0x7fffffff or min(sizes) < -0x80000000:
+        raise ValueError(f"{sizes}: a size or place past 32 bits")
+
+
 def make_gated_shape(B: int, N: int, H: int, D: int = HEAD_DIM, io_dtype: str = "bf16",
                      scale: float = 1.0) -> LaGatedShape:
     io = {"bf16": LA_IO_BF16, "f32": LA_IO_F32, "float32": LA_IO_F32}[io_dtype]
+    _fit(B, N, H, D)
     return LaGatedShape(int(B), int(N), int(H), int(D), io, float(scale))
 
 
@@ -305,6 +312,7 @@ def la_rotary(shape: LaRotaryShape, Q, K, positions, Qo, Ko, stream=None) -> Non
 def make_norm_shape(B: int, N: int, C: int, io_dtype: str = "bf16", norm: str = "layer",
                     eps: float = 1e-6, alpha: float = 1.0) -> LaNormShape:
     io = {"bf16": LA_IO_BF16, "f32": LA_IO_F32, "float32": LA_IO_F32}[io_dtype]
+    _fit(B, N, C)
     return LaNormShape(int(B), int(N), int(C), io, {"rms": 0, "layer": 1}[norm], float(eps),
                        float(alpha))
 
@@ -549,6 +557,7 @@ def _gated_shape(Q, K, V, G, scale, **states) -> LaGatedShape:
     io = _io_of(Q, "Q")
     full, device = Q.shape, Q.get_device()
     B, N, H, D = full
+    _fit(*full)
     _need("Q", Q, full, Q.dtype, device)
     _need("K", K, full, Q.dtype, device)
     _need("V", V, full, Q.dtype, device)
@@ -623,7 +632,9 @@ def make_rotary_shape(B: int, N: int, H: int, Hk: int, D: int, io_dtype: str = "
             raise ValueError(f"scaling {scaling!r}: wrong number of values")
         if kind == 3:
             length, slow, fast = scaling[2:]
-    return LaRotaryShape(B, N, H, Hk, D, D if rot is None else rot, io, _ROTARY_LAYOUTS[layout], kind,
+    rot = D if rot is None else rot
+    _fit(B, N, H, Hk, D, rot, offset)
+    return LaRotaryShape(B, N, H, Hk, D, rot, io, _ROTARY_LAYOUTS[layout], kind,
                          int(inverse), int(pos_rows), offset, base, factor, length, slow, fast, mscale)
 
 
@@ -680,6 +691,7 @@ def _norm_shape(x, f, gate, w_post, w_pre, mod_scale, mod_shift, norm, eps, alph
     io = _io_of(x, "x")
     full, device = x.shape, x.get_device()
     B, N, C = full
+    _fit(B, N, C)
     _need("x", x, full, x.dtype, device)
     _need("f", f, full, x.dtype, device)
     for name, t in like_x.items():

@@ -83,3 +83,25 @@ def test_binding_refuses_what_does_not_fit():
     for bad in (dict(layout="third"), dict(scaling=("cubic", 2.0))):
         with pytest.raises(KeyError):
             la.rotary(q, **bad)
+
+
+def test_sizes_past_32_bits_are_refused():
+    """A C int would keep their low 32 bits: 2^32 + 5 tokens would be 5."""
+    big = 2 ** 32 + 5
+    for bad in (dict(offset=big), dict(rot=2 ** 32 + 32), dict(offset=-big)):
+        with pytest.raises(ValueError, match="32 bits"):
+            la.make_rotary_shape(1, 4, 2, 2, 32, **bad)
+    for make, args in ((la.make_rotary_shape, (1, big, 2, 2, 32)), (la.make_gated_shape, (1, big, 2)),
+                       (la.make_gated_shape, (big, 1, 2)), (la.make_norm_shape, (1, big, 64)),
+                       (la.make_norm_shape, (1, 1, big))):
+        with pytest.raises(ValueError, match="32 bits"):
+            make(*args)
+    f, e = torch.float32, torch.empty
+    with pytest.raises(ValueError, match="32 bits"):
+        la.gated_attention(*[e((1, big, 0, 32), dtype=f)] * 3, e((1, big, 0), dtype=f))
+    with pytest.raises(ValueError, match="32 bits"):
+        la.rotary(e((1, big, 0, 32), dtype=f))
+    with pytest.raises(ValueError, match="32 bits"):
+        la.rotary(e((1, 2, 2, 32), dtype=f), offset=big)
+    with pytest.raises(ValueError, match="32 bits"):
+        la.gate_residual_norm(e((0, big, 64), dtype=f))
