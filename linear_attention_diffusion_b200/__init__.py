@@ -522,6 +522,8 @@ def _on(stream, x):
     if isinstance(stream, int):
         stream = (torch.cuda.ExternalStream(stream, device=device) if stream
                   else torch.cuda.default_stream(device))
+    elif stream.device.index != device:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to GPU {device}")
     return torch.cuda.stream(stream)
 
 

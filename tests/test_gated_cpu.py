@@ -189,3 +189,16 @@ def test_launches_follow_the_cut():
     assert b(1, 16384, 70) == 4 and b(64, 4096, 70) == 2 and b(1, 3, 2) == 2
     assert f(2, 0, 3) == 0 and b(0, 9, 3) == 0 and f(1, 4, 2, 64) == 0 and b(-1, 4, 2) == 0
 
+
+
+def test_a_stream_of_another_gpu_is_refused():
+    """The call would run on the current stream of the tensors' GPU, not on the one given."""
+    from types import SimpleNamespace
+    x = SimpleNamespace(is_cuda=True, get_device=lambda: 0, device=torch.device("cuda:0"))
+    stream = SimpleNamespace(device=torch.device("cuda:1"))
+    for call in (lambda: la.gated_attention(x, x, x, x, stream=stream),
+                 lambda: la.gated_attention_backward(x, x, x, x, x, stream=stream),
+                 lambda: la.rotary(x, stream=stream), lambda: la.gate_residual_norm(x, stream=stream),
+                 lambda: la.gate_residual_norm_backward(x, None, x, None, stream=stream)):
+        with pytest.raises(ValueError, match="belongs to cuda:1"):
+            call()
