@@ -276,7 +276,8 @@ la_status la_qkv_state(const la_shape* shape, int C, const void* X,
  * [B, N, H, D] tensors of io_dtype, G and its gradient dense [B, N, H] float32,
  * states dense [B, H, D, D] float32 (row: dimension of k, column: of v). */
 typedef struct {
-  int B, N, H;  /* batch elements, tokens, heads; >= 0 */
+  int B, N, H;  /* batch elements, tokens, heads; >= 0, B and H <= 65535, B H <= 2^24,
+                   N <= 2^30, B N H < 2^35 */
   int D;        /* head width; must be 32 */
   int io_dtype; /* LA_IO_BF16 or LA_IO_F32 */
   float scale;  /* factor of the queries, finite */
@@ -298,14 +299,22 @@ int la_gated_launches(const la_gated_shape* shape, int backward);
  * norm to o after. G holds the log gates g <= 0. A gate below -104 (-inf
  * included) lets nothing through: the state starts anew at that token, which
  * packs several sequences into one row (the first token of each has g = -inf).
- * Larger gates are summed as they are, g > 0 lets the state grow. S_in NULL: a
+ * Larger gates are summed as they are; g > 0 lets the state grow, as long as the
+ * decay over any run of tokens stays within float32's range. S_in NULL: a
  * zero state. S_out (may be NULL) receives the last state; it may be S_in
  * itself, so a sequence can be fed in pieces of any length (prompt, then one
  * token at a time). N = 0 copies S_in to S_out. A NaN or infinity in q, k, v or
  * G may reach the outputs of all tokens of its 16-token block and of later ones (in the
  * backward, where dO counts too, also of earlier ones), but never passes a gate that lets
  * nothing through: what is packed before and behind it stays as it is.
- * float32 sums and state; bf16 outputs are rounded once. Up to 4 tokens run as
+ * float32 sums and state. In products, what the kernels compute (states, decayed
+ * keys, masked weights) keeps 24 bits where a float32 output depends on it (S_out,
+ * and all outputs of float32 tensors) and 17 bits where only a bf16 O does: O is off
+ * by half a bf16 step, its own rounding, and by at most 2^-15 of the sum of its
+ * terms' sizes (and 2^-22 for every 16 tokens that a term has crossed), so about one
+ * number in 300 is the other neighbour of the exact one.
+ * For calls of more than 4 tokens O's bits may depend on whether S_out is given (the
+ * state's updates then keep 24 bits). Up to 4 tokens run as
  * one launch that walks them one by one; longer calls walk 16-token blocks on
  * the tensor cores, in one launch where the rows are short or B*H fills the GPU,
  * else in three (segments' states, their combination, the segments). Deterministic.
@@ -321,10 +330,11 @@ la_status la_gated_attention(const la_gated_shape* shape, const void* Q, const v
  *   dq_n = scale S_n dO_n,  dk_n = U_n v_n,  dv_n = k_n U_n,
  *   dg_n = <exp(g_n) U_n, S_{n-1}>,  dS_in = exp(g_0) U_0.
  * dQ, dK, dV: io_dtype; dG: [B,N,H] float32 (0 at gates below -104); dS_in: [B,H,D,D]
- * float32 or NULL. S_in as the forward had it (S_out must not have been written
- * over it). Recomputes the states; two launches, four where the sequence is cut
- * into segments. Deterministic. No output may overlap another, an input or the
- * workspace. */
+ * float32 or NULL. Products keep 24 bits for dG, dS_in, dQ and dK (whose row sums make
+ * dG) and 17 for a bf16 dV, as in the forward. S_in as the forward had it (S_out must
+ * not have been written over it). Recomputes the states; two launches, four where the
+ * sequence is cut into segments. Deterministic. No output may overlap another, an input
+ * or the workspace. */
 la_status la_gated_attention_backward(const la_gated_shape* shape, const void* Q, const void* K,
                                       const void* V, const float* G, const float* S_in,
                                       const void* dO, const float* dS_out, void* dQ, void* dK,
@@ -343,8 +353,8 @@ la_status la_gated_attention_backward(const la_gated_shape* shape, const void* Q
  *                        (fast - slow), 0, 1), t = original_length f_k / 2 pi: the turns
  *                        that the pair makes over the original length */
 typedef struct {
-  int B, N;
-  int H, Hk;    /* heads of Q and of K; Hk = 0: there is no K */
+  int B, N;     /* >= 0, B N < 2^31 */
+  int H, Hk;    /* heads of Q and of K, (H + Hk) D < 2^24; Hk = 0: there is no K */
   int D;        /* head width: a multiple of 8 in [8, 256] */
   int rot;      /* even, 0 <= rot <= D */
   int io_dtype; /* LA_IO_BF16 or LA_IO_F32 */
@@ -371,7 +381,7 @@ la_status la_rotary(const la_rotary_shape* shape, const void* Q, const void* K,
  * the block and a norm before the next one. x, f, h, y and their gradients are dense
  * [B, N, C] tensors of io_dtype; parameters are float32, dense. */
 typedef struct {
-  int B, N;
+  int B, N;     /* >= 0, B <= 65535, N <= 2^30, B N C < 2^40 */
   int C;        /* a multiple of 8 in [8, 8192] */
   int io_dtype; /* LA_IO_BF16 or LA_IO_F32 */
   int norm;     /* of y: 0 RMS, 1 layer (the mean is subtracted) */

@@ -573,7 +573,8 @@ def gated_attention(Q, K, V, G, S_in=None, scale: float = 1.0, want_state: bool 
                     stream=None):
     """O (and the last state when ``want_state`` or ``S_out`` is given) of gated linear attention:
     S_n = exp(g_n) S_{n-1} + k_n^T v_n, o_n = scale q_n S_n, for [B, N, H, 32] CUDA tensors and
-    log gates G [B, N, H] float32. ``S_out`` may be ``S_in``: the state is then updated in place."""
+    log gates G [B, N, H] float32. ``S_out`` may be ``S_in``: the state is then updated in place.
+    bf16 tensors: the state keeps 24 bits, what only O depends on 17 (see include/la.h)."""
     if stream is not None:
         with _on(stream, Q):
             return gated_attention(Q, K, V, G, S_in, scale, want_state, S_out)

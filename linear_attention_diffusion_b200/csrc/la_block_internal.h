@@ -10,7 +10,7 @@
 
 namespace la {
 
-// Gated linear attention (la_gated.cu, la_gated_backward.cu).
+// Gated linear attention (la_gated.cu, la_gated.cuh).
 struct GatedProblem {
   int B, N, H;
   int io;       // 0 bf16, 1 float32

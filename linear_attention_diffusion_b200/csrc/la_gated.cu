@@ -19,8 +19,9 @@
 // segments a row are enough, one CTA takes a row and does all three in one launch.
 //
 // What bounds it, at 16384 tokens of 70 heads in bf16 (294 MB that it cannot do without,
-// 46 us): the first pass reads 147 MB in 41 us, of which a copy of its pattern takes 30; the
-// walk moves 294 MB in 67 us, the pattern alone 57. Neither the tensor cores (50 products a
+// 46 us; 109 us a call with the last state, 107 without): the first pass reads 147 MB in 42 us
+// (34 without the last state, see segment_pass), of which a copy of its pattern takes 30; the
+// walk moves 294 MB in 68 us, the pattern alone 57. Neither the tensor cores (50 products a
 // block of the walk, 26 us), nor the schedulers (390 instructions a block, 23 us) nor HBM is full:
 // with 8 to 12 warps an SM, as many as the registers allow, products and the arithmetic
 // between them overlap only in part. More warps with fewer registers spill, and blocks of 16
@@ -36,7 +37,7 @@
 // backwards that carries U. dg is summed backwards from the two walks' float32 row
 // products, and set afresh to <U, S> every kGateAnchor tokens, where the first walk
 // has left its S: rounding errors of the sum do not grow with the length. At the size above
-// the four launches take 72, 9, 93 and 134 us; the walk backwards issues 114 products and 760
+// the four launches take 76, 6, 98 and 143 us by themselves; the walk backwards issues 114 products and 760
 // instructions a block, together 108 us if nothing overlapped.
 #include "la_gated.cuh"
 #include "la_sm100.cuh"
@@ -504,7 +505,8 @@ walk_back_kernel(const Walk a) {
 // its X to slot s - 1 of `grads`. It walks a segment from its end: what it reads last, the
 // segments' first tokens, the walk reads first, while it is still in L2. Once the decay to
 // the segment's end has become 0, no earlier token has a part in S.
-// kExact as in the walk: 16384 tokens of 70 heads take 41 us, with 17 bits 32 us.
+// kExact as in the walk: 16384 tokens of 70 heads take 42 us, with 17 bits (a forward whose last
+// state nobody asks for) 34 us.
 template <int NP, bool kBack, bool kExact, int kStages>
 __device__ __forceinline__ void segment_pass(const GatedProblem& p, const Place<kBlocks<NP>>& at,
                                              const void* qv, const void* kv, const void* vv,
@@ -620,8 +622,9 @@ segment_kernel(const GatedProblem p, int segs, const void* qv, const void* kv, c
 
 // A whole row in one CTA: its warps take the segments of one head, leave the segments' own
 // states in shared memory, and each adds up those before its own. K and V come from L2 the
-// second time, and nothing of a second or third launch is left. Four warps: 8 x 509 tokens of
-// 36 heads in bf16 take 15.3 us (two warps 19.6, six 15.8, three launches 20.5).
+// second time, and nothing of a second or third launch is left. 8 x 509 tokens of 36 heads in
+// bf16 take 19.3 us in a graph, three launches 23.9; two warps instead of four took 1.28 times as
+// long, six 1.03 times.
 constexpr int kRowWarps = 4;
 template <int NP>
 struct RowSmem {
@@ -959,25 +962,28 @@ cudaError_t backward(const GatedProblem& p, const void* Q, const void* K, const 
 }  // namespace gated
 
 // Segments of a row. Cutting costs a second reading of K and V (and Q and dO backwards) and
-// three launches more, so heads that fill half the GPU by themselves are not cut. Otherwise:
+// two launches more, so heads that fill half the GPU by themselves are not cut. 2500 tokens of 900
+// heads, bf16: 155 us whole, 197 cut in two (880 heads: 152 and 172, 1700 heads: 253 and 326),
+// backwards 544 and 699; 1500 tokens of 760 heads, float32: 254 and 274, backwards 692 and 753.
+// Otherwise:
 //  - as many segments as give every warp's place on 148 SMs one, by registers (bf16: 168 a
 //    thread forwards, 255 backwards) or shared memory (float32). 16384 tokens of 70 heads, bf16:
-//    100 us, with twice the segments 112 us.
+//    109 us, with twice the segments 118 us.
 //  - float32 is bound by its many products, and its warps, more of them, level out better in
-//    four waves: 276 us against 348 us there, 756 against 867 us backwards.
+//    four waves: 289 us against 291 us there, 742 against 852 us backwards.
 //  - no segment so short that its start and its state cost more than its work: 64 tokens
-//    (1024 tokens of 36 heads: 10.7 us, with 32 tokens 11.8 us), 96 for much float32 work (8 x
-//    509 tokens of 36 heads: 43 us, with 64 tokens 45 us); where little is to be done at all, the
+//    (1024 tokens of 36 heads: 11.8 us, with 32 tokens 13.1 us), 96 for much float32 work (1024
+//    tokens of 140 heads: 46.6 us, with 64 tokens 49.2 us); where little is to be done at all, the
 //    time is one warp's, and 32 tokens are best (256 tokens of 36 heads: 7.0 us, with 64 tokens
 //    8.9 us), up to a number of segments whose combination would take longer (4000 tokens of 4
-//    heads, float32 backwards: 37 us with 125 segments, 63 us with 32).
+//    heads, float32 backwards: 39 us with 125 segments, 62 us with 32).
 //
 // Forwards, a CTA takes a whole row where its four warps are enough: short rows, or rows of
 // so many heads that they would not be cut much finer. In one launch against three, bf16: 256
-// tokens of 70 heads 6.9 and 7.6 us (512 tokens: 10.9 and 10.0), 1024 tokens of 140 heads 19.2
-// and 21.1 us (2048: 35.8 and 33.9), 2000 tokens of 630 heads 132 and 144 us (4096 of 280: 111
-// and 103). float32, whose warps are fewer: 1024 tokens of 280 heads 70 and 76 us (of 140: 47 and
-// 46), 64 tokens 9.0 and 12.0 us; more heads than one wave of CTAs: 333 and 285 us (630 heads).
+// tokens of 70 heads 6.8 and 7.9 us (512 tokens: 12.3 and 11.1), 1024 tokens of 140 heads 21.9
+// and 23.5 us (2048: 39.5 and 37.1), 2000 tokens of 630 heads 140 and 145 us (4096 of 280: 128
+// and 114). float32, whose warps are fewer: 1024 tokens of 280 heads 68 and 78 us (of 140: 47 and
+// 46), 64 tokens 8.2 and 9.9 us; more heads than one wave of CTAs: 172 and 163 us (630 heads).
 void gated_split(GatedProblem& p, bool backward) {
   const long long BH = 1LL * p.B * p.H, work = BH * p.N;
   const bool bf16 = p.io == LA_IO_BF16;

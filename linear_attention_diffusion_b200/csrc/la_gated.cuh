@@ -18,7 +18,10 @@
 // keep all 24. bf16 tensors are one part. What the kernels compute (states,
 // decayed keys, masked weights) enters with two parts where only a bf16 output depends
 // on it, with three where a float32 one does (the state, the gates' gradient) and for
-// float32 tensors; every sum is float32.
+// float32 tensors; every sum is float32. Two parts where a bf16 output follows: one output in
+// 300 then rounds to the other neighbour (three parts: one in 4000), the error against 64 bits
+// is 1.66e-3 of the 2-norm either way, the output's own rounding, and 32760 tokens of 70 heads
+// take 213 us instead of 252, 8 x 509 tokens of 36 heads 19 instead of 25.
 #pragma once
 
 #include <cuda_bf16.h>

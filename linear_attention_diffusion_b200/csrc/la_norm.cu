@@ -20,9 +20,13 @@
 // same bits every time.
 //
 // 16384 x 2240 in bf16 with gate and modulation: forward 53 us, 5.5 TB/s (the warps' next rows
-// ahead in registers or in L2, or a CTA per row, measured slower: 58 to 71 us); backward 88 us,
-// 5.0 TB/s, of which the column sums' second kernel is 8: three sums over a row, each its shuffles
-// and a barrier, run beside the copies of the next row.
+// ahead in registers or in L2, or a CTA per row, measured slower: 58 to 71 us); backward 90 us,
+// 4.9 TB/s, of which the column sums' second kernel is 8: three sums over a row, each its shuffles
+// and a barrier, run beside the copies of the next row. Of the measured copy's rate, as many bytes
+// of other widths take, forward: 84 to 86 % at 1152 to 2304 columns (float32 80 %), 62 to 66 % at
+// 2560 to 4096 (76 to 82 %), 44 and 51 % at 5120 and 8192 (60 and 66 %). Backward: 74 to 81 % up to
+// 2560 columns, 47 % at 2816, 62 to 70 % at 4096 to 8192; float32, whose rows are twice as long for
+// a thread's registers, 53 % and 45 to 49 %.
 #include "la_block_internal.h"
 #include "la_common.cuh"
 #include "la_sm100.cuh"
@@ -272,7 +276,8 @@ norm_kernel(const NormProblem p, const T* x, const T* f, const NormParams w, T* 
 // A backward thread owns two vectors of every row: the sums over a row cost each thread its
 // shuffles and a barrier, which 16 columns pay for better than 8. The next row is on its way
 // to shared memory meanwhile, every thread its own pieces, so nothing but the thread waits
-// for them; in registers they would spill its column sums.
+// for them; in registers they would be 32 to 64 more of the 128 that a thread has, which do not
+// hold all of a row's arithmetic as it is: bf16 spills 12 to 80 bytes, float32 24 to 236.
 constexpr int kBackVecs = 2, kNarrow = 160, kWide = 512;
 static_assert(kWide * kBackVecs * kVec == kNormMaxC, "the widest row");
 
@@ -593,7 +598,10 @@ cudaError_t run_forward(const NormProblem& p, int threads, const void* x, const 
 }
 
 // A warp takes a row of up to 9 vectors per lane (2304 columns) where the rows fill the GPU;
-// few or long rows get whole CTAs, a vector per thread.
+// few or long rows get whole CTAs, a vector per thread. bf16, a warp and a CTA a row: 2240 columns,
+// 154 rows 4.9 and 3.8 us, 600 rows 6.5 and 6.9, 1184 rows 8.0 and 8.9, 9600 rows 34 and 41; 1152
+// columns, 154 rows 3.6 and 2.9, 1184 rows 5.5 and 6.7 (float32 7.0 and 8.0). Wider rows have the
+// second form alone.
 template <typename T>
 cudaError_t forward(const NormProblem& p, const void* x, const void* f, const NormParams& w,
                     void* h, void* y, cudaStream_t s) {
@@ -646,8 +654,9 @@ cudaError_t backward(const NormProblem& p, const void* x, const void* f, const N
 
 }  // namespace
 
-// CTAs of a batch element in the backward: enough warps for the GPU (by registers), but at
-// least 8 rows each, so that the partial column sums stay a tenth of the traffic.
+// CTAs of a batch element in the backward: enough warps for the GPU (by registers; above 2560
+// columns one CTA an SM), but at least 8 rows each: at 8 rows of bf16 the partial column sums,
+// written and read back, are a quarter of the rows' bytes, of float32 an eighth.
 void norm_split(NormProblem& p) {
   const int threads = backward_threads(p.C);
   const long long per_sm = threads <= kNarrow ? 480 / threads : 1;

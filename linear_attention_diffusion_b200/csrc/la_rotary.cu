@@ -28,8 +28,9 @@ constexpr int kThreads = 128;
 constexpr int kFlight = 2;  // items in flight per thread
 enum { kInterleaved = 0, kHalves = 1, kHalvesScalar = 2 };
 
-// Division of numbers below 2^31 by a divisor the host knows: a high product and shifts (a
-// number's place in the tensors takes two divisions, as many instructions as its rotation).
+// Division of numbers below 2^31 by a divisor the host knows, by the round-up method for invariant
+// divisors (Granlund and Montgomery 1994): a high product and a shift (a number's place in the
+// tensors takes two divisions, as many instructions as its rotation).
 struct Divide {
   uint32_t d, m, shift;
   static Divide by(uint32_t d) {
