@@ -585,7 +585,8 @@ __device__ __forceinline__ void segment_pass(const GatedProblem& p, const Place<
         X.template update<NP, NB, 3, kStops>(w0 * w1, x, y, w);
         if (kStops && bad_x != 0 && spoils_start(bad_x, stops)) X.spoil();
       }
-      total *= w0 * w1;
+      // a stop on either side of a gate that is no number leaves 0, not NaN
+      total = total == 0.0f || w0 * w1 == 0.0f ? 0.0f : total * (w0 * w1);
     };
     run_step<NP, NB>(gate, false, lane, step);
     if (!kBack && total == 0.0f) break;

@@ -379,3 +379,46 @@ def test_gate_gradients_window_by_window(cuda_device, io, gates, B, N, H):
     ref = orc.gated_attention_backward(*cut, 0.4)[3]
     err = orc.gated_window_errors(dG[:, :, some].cpu(), ref)
     assert err.max() <= 2.0 ** -15, err.max()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("B,N,H,seed", [(1, 61, 3, 1), (2, 333, 5, 2), (3, 1000, 2, 3), (1, 40, 900, 4), (1, 700, 70, 5)])
+def test_packed_sequences_are_apart(cuda_device, io, B, N, H, seed):
+    """Rows packed from sequences of 1 to some 40 tokens, with numbers that are not finite strewn
+    over them: every sequence without one, and the states at its ends, is what it would be alone."""
+    q, k, v, g, do, S0, dS = _draw(B, N, H, io, seed)
+    r = torch.Generator().manual_seed(seed + 100)
+    stop = torch.rand((B, N, H), generator=r) < 0.08
+    bad = torch.rand((B, N, H), generator=r) < 0.02
+    kind = torch.randint(0, 5, (B, N, H), generator=r)
+    g[stop] = -float("inf")
+    clean = [x.clone() for x in (q, k, v, g, do)]
+    for i, x in enumerate((q, k, v, do)):
+        x[..., i][bad & (kind == i)] = float("nan") if seed % 2 else float("inf")
+        clean[i if i < 3 else 4][bad & (kind == i)] = 0
+    g[bad & (kind == 4) & ~stop] = float("nan")
+    number = stop.long().cumsum(1)                              # of each token's sequence in its row
+    spoiled = torch.zeros((B, N + 1, H), dtype=torch.long).scatter_add_(1, number, bad.long()) > 0
+    fine = ~spoiled.gather(1, number)
+    assert 0.2 < fine.float().mean() < 0.95
+    first, last = ~spoiled[:, 0], fine[:, -1]                   # the states' sequences, [B, H]
+    tol = _tol(io, N)
+
+    def check(name, got, ref, mag, tol, half, ok):
+        got, ok = orc.to_f64(got.cpu()), ok.numpy()
+        err, bound = np.abs(got - ref)[ok], (half * np.abs(ref) + tol * mag + 1e-36)[ok]
+        assert np.isfinite(got[ok]).all() and (err <= bound).all(), name
+
+    dev = _dev(q, k, v, g)
+    O, S = la.gated_attention(*dev, S_in=S0.cuda(), want_state=True)
+    ref, S_ref = orc.gated_attention(*clean[:4], S0)
+    A, AS = orc.gated_magnitudes(*clean[:4], S_in=S0)
+    check("O", O, ref, A, tol, HALF[io], fine)
+    check("S", S, S_ref, AS, tol, HALF["f32"], last)
+    check("O alone", la.gated_attention(*dev, S_in=S0.cuda()), ref, A, tol, HALF[io], fine)
+    got = la.gated_attention_backward(*dev, do.cuda(), S_in=S0.cuda(), dS_out=dS.cuda())
+    refs = orc.gated_attention_backward(*clean, S0, dS)
+    mags = orc.gated_magnitudes(*clean, S0, dS)
+    for i, name in enumerate(("dQ", "dK", "dV", "dG")):
+        check(name, got[i], refs[i], mags[i], 2 * tol, HALF[io] if i < 3 else HALF["f32"], fine)
+    check("dS_in", got[4], refs[4], mags[4], tol, HALF["f32"], first)
