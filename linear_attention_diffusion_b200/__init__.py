@@ -264,16 +264,17 @@ def la_qkv_state(shape: LaShape, C: int, X, W, bias, Q, S, z, ws, stream=None) -
            "la_qkv_state")
 
 
-def _fit(*sizes: int) -> None:
-    """Raise ValueError for a number that a C int would cut to its low 32 bits."""
-    if max(sizes) > 0x7fffffff or min(sizes) < -0x80000000:
-        raise ValueError(f"{sizes}: a size or place past 32 bits")
+def _unfit(*sizes: int) -> ValueError:
+    """For numbers that a C int would cut to their low 32 bits. Found by the callers with an or of
+    all of them and one shift, which leaves 0, or -1 where one is negative, if all fit."""
+    return ValueError(f"{sizes}: a size or place past 32 bits")
 
 
 def make_gated_shape(B: int, N: int, H: int, D: int = HEAD_DIM, io_dtype: str = "bf16",
                      scale: float = 1.0) -> LaGatedShape:
     io = {"bf16": LA_IO_BF16, "f32": LA_IO_F32, "float32": LA_IO_F32}[io_dtype]
-    _fit(B, N, H, D)
+    if (B | N | H | D) >> 31 not in (0, -1):
+        raise _unfit(B, N, H, D)
     return LaGatedShape(int(B), int(N), int(H), int(D), io, float(scale))
 
 
@@ -312,7 +313,8 @@ def la_rotary(shape: LaRotaryShape, Q, K, positions, Qo, Ko, stream=None) -> Non
 def make_norm_shape(B: int, N: int, C: int, io_dtype: str = "bf16", norm: str = "layer",
                     eps: float = 1e-6, alpha: float = 1.0) -> LaNormShape:
     io = {"bf16": LA_IO_BF16, "f32": LA_IO_F32, "float32": LA_IO_F32}[io_dtype]
-    _fit(B, N, C)
+    if (B | N | C) >> 31 not in (0, -1):
+        raise _unfit(B, N, C)
     return LaNormShape(int(B), int(N), int(C), io, {"rms": 0, "layer": 1}[norm], float(eps),
                        float(alpha))
 
@@ -559,7 +561,8 @@ def _gated_shape(Q, K, V, G, scale, **states) -> LaGatedShape:
     io = _io_of(Q, "Q")
     full, device = Q.shape, Q.get_device()
     B, N, H, D = full
-    _fit(*full)
+    if (B | N | H) >> 31:
+        raise _unfit(B, N, H)
     _need("Q", Q, full, Q.dtype, device)
     _need("K", K, full, Q.dtype, device)
     _need("V", V, full, Q.dtype, device)
@@ -636,7 +639,8 @@ def make_rotary_shape(B: int, N: int, H: int, Hk: int, D: int, io_dtype: str = "
         if kind == 3:
             length, slow, fast = scaling[2:]
     rot = D if rot is None else rot
-    _fit(B, N, H, Hk, D, rot, offset)
+    if (B | N | H | Hk | D | rot | offset) >> 31 not in (0, -1):
+        raise _unfit(B, N, H, Hk, D, rot, offset)
     return LaRotaryShape(B, N, H, Hk, D, rot, io, _ROTARY_LAYOUTS[layout], kind,
                          int(inverse), int(pos_rows), offset, base, factor, length, slow, fast, mscale)
 
@@ -694,7 +698,8 @@ def _norm_shape(x, f, gate, w_post, w_pre, mod_scale, mod_shift, norm, eps, alph
     io = _io_of(x, "x")
     full, device = x.shape, x.get_device()
     B, N, C = full
-    _fit(B, N, C)
+    if (B | N | C) >> 31:
+        raise _unfit(B, N, C)
     _need("x", x, full, x.dtype, device)
     _need("f", f, full, x.dtype, device)
     for name, t in like_x.items():
