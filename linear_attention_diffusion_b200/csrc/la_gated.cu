@@ -233,8 +233,8 @@ __device__ __forceinline__ void walk_pass(const Walk& a, const Place<kBlocks<NP>
         __syncwarp();
       }
       const Decay<NP, NB> d = decays<NP, NB, kStops>(known, gate, stops, lane);
-      const float head = d.template head<kStops>(lane), tail = d.template tail<kStops, kLow>(lane);
-      const float whole = d.template whole<kStops>(lane);
+      const float head = d.template head<kStops, kLow>(lane), tail = d.template tail<kStops, kLow>(lane);
+      const float whole = d.template whole<kStops, kLow>(lane);
       // decays of the step's blocks, from its start and to its end
       const float w0 = __shfl_sync(0xffffffffu, whole, 0);
       const float w1 = NB == 1 ? 1.0f : __shfl_sync(0xffffffffu, whole, 16);
@@ -397,8 +397,8 @@ walk_back_kernel(const Walk a) {
         __syncwarp();
       }
       const Decay<NP, NB> d = decays<NP, NB, kStops>(known, gate, stops, lane);
-      const float head = d.template head<kStops>(lane), tail = d.template tail<kStops, kLow>(lane);
-      const float whole = d.template whole<kStops>(lane);
+      const float head = d.template head<kStops, kLow>(lane), tail = d.template tail<kStops, kLow>(lane);
+      const float whole = d.template whole<kStops, kLow>(lane);
       const float w0 = __shfl_sync(0xffffffffu, whole, 0);
       const float w1 = NB == 1 ? 1.0f : __shfl_sync(0xffffffffu, whole, 16);
       const float to_end = NB == 2 && lane < 16 ? tail * w1 : tail;
@@ -555,7 +555,7 @@ __device__ __forceinline__ void segment_pass(const GatedProblem& p, const Place<
         __syncwarp();
       }
       const Decay<NP, NB> d = decays<NP, NB, kStops>(known, gate, stops, lane);
-      const float whole = d.template whole<kStops>(lane);
+      const float whole = d.template whole<kStops, kLow>(lane);
       const float w0 = __shfl_sync(0xffffffffu, whole, 0);
       const float w1 = NB == 1 ? 1.0f : __shfl_sync(0xffffffffu, whole, 16);
       float w[NB][4];
@@ -573,7 +573,7 @@ __device__ __forceinline__ void segment_pass(const GatedProblem& p, const Place<
         if (kStops && bad != 0 && spoiled_from(bad, stops, kStep - 1) != 0.0f) S.spoil();
       }
       if (kBack) {
-        const float head = d.template head<kStops>(lane);
+        const float head = d.template head<kStops, kLow>(lane);
         const float from_start = (NB == 2 && lane >= 16 ? head * w0 : head) * p.scale;
         Frag<NP> x[NB], y[NB];
 #pragma unroll
@@ -792,8 +792,9 @@ step_kernel(const GatedProblem p, const T* Q, const T* K, const T* V, const floa
   }
   for (int n = 0; n < p.N; ++n) {
     const size_t at = base + static_cast<size_t>(n) * p.H * 32;
-    const float g = G[gbase + static_cast<size_t>(n) * p.H] * kLog2e;
-    const float a = g < kStop ? 0.0f : exp2_fast(g);
+    const float g = G[gbase + static_cast<size_t>(n) * p.H], g2 = g * kLog2e;
+    const float a = g2 < kStop ? 0.0f
+                               : Decay<1, 1>::template power<true>(g2, fmaf(g, kLog2e, -g2) + g * kLog2eRest);
     const float k = to_f(K[at + lane]), q = to_f(Q[at + lane]) * p.scale;
     float v[4], o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     load4(V + at + e4, v);

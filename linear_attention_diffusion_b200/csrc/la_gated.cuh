@@ -45,7 +45,8 @@ struct Io<3> {
 };
 
 constexpr int kPlane = kGateBlock * 64;  // bytes of 16 tokens x 32 bf16
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f;     // rounded, and
+constexpr float kLog2eRest = 1.925963033500012e-8f;  // the rest of it
 // A gate whose decay 2^x is below the smallest float32 lets nothing through:
 // it is kept apart from the sums of the others, where it would cost their
 // precision (and -inf would give NaN).
@@ -611,8 +612,8 @@ __device__ __forceinline__ void scale_row(float (&acc)[4][4], int h, float f) {
 // log2 gates from its block's first token to it, stops left out.
 //
 // A decay is the difference of two such sums. Where a sum falls below kEasy (and always for
-// float32 tensors) the sums carry what their rounding left in `low`, so that gates of -100 do
-// not cost the small gates next to them their low bits; above it the difference is good to
+// float32 tensors) the sums carry what their rounding left in `low`, so that gates of -100 cost
+// neither the small gates next to them nor what passes them low bits; above it the difference is good to
 // 2^-18 (sums of gates that let the state grow, to 2^-24 of their size). Where a bf16 step is
 // `hard`, for that or for a stop, it runs a second copy of the step's code that minds both, so
 // that the ordinary one stays free of branches, one long stretch in which the scheduler can lay
@@ -644,6 +645,7 @@ struct Decay {
     hard = wide || stops != 0;
     if (wide) {
       x = x0;
+      if (x0 != 0.0f) low = fmaf(g, kLog2e, -x0) + g * kLog2eRest;
 #pragma unroll
       for (int d = 1; d < 16; d <<= 1) {
         const float y = __shfl_up_sync(0xffffffffu, x, d, 16);
@@ -663,10 +665,16 @@ struct Decay {
   __device__ __forceinline__ uint32_t own_stops(int lane) const {
     return NB == 1 ? stops : (stops >> (lane & 16)) & 0xffffu;
   }
+  // 2^(x + rest)
+  template <bool kLow>
+  static __device__ __forceinline__ float power(float x, float rest) {
+    const float f = exp2_fast(x);
+    return kLow ? fmaf(f, rest * 0.6931471805599453f, f) : f;
+  }
   // from the state before the lane's block to its token
-  template <bool kStops>
+  template <bool kStops, bool kLow>
   __device__ __forceinline__ float head(int lane) const {
-    const float f = exp2_fast(c);
+    const float f = power<kLow>(c, low);
     return kStops && (own_stops(lane) & ((2u << (lane & 15)) - 1u)) ? 0.0f : f;
   }
   // from the lane's token to its block's end
@@ -676,9 +684,9 @@ struct Decay {
     return kStops && (own_stops(lane) >> ((lane & 15) + 1)) ? 0.0f : f;
   }
   // over the whole of the lane's block
-  template <bool kStops>
+  template <bool kStops, bool kLow>
   __device__ __forceinline__ float whole(int lane) const {
-    return kStops && own_stops(lane) ? 0.0f : exp2_fast(last);
+    return kStops && own_stops(lane) ? 0.0f : power<kLow>(last, last_low);
   }
   // of `x`, one value per token: the values of tokens 16 b + 2 (l % 4) + {0, 1, 8, 9}
   static __device__ __forceinline__ void spread(float x, int b, int lane, float (&out)[4]) {

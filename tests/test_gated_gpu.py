@@ -422,3 +422,28 @@ def test_packed_sequences_are_apart(cuda_device, io, B, N, H, seed):
     for i, name in enumerate(("dQ", "dK", "dV", "dG")):
         check(name, got[i], refs[i], mags[i], 2 * tol, HALF[io] if i < 3 else HALF["f32"], fine)
     check("dS_in", got[4], refs[4], mags[4], tol, HALF["f32"], first)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [1, 3, 9, 16])
+def test_what_passes_strong_gates_keeps_its_bits(cuda_device, io, N):
+    """Without keys the state is a product of decays times the one before. Bound 2^-20 relative: an
+    exponential of 2^-22 and a few float32 roundings, for each of up to three tokens of their own or
+    for a block of 16; a rounded exponent of 2^7 alone would be off by 2^-18. It holds for normal
+    numbers: below 2^-126 a step of float32 is 2^-149, whatever the number. Backwards the same for
+    the gradient of the first state."""
+    r = torch.Generator().manual_seed(4)
+    B, H = 4, 60
+    q, do = (torch.randn((B, N, H, D), generator=r).to(torch.bfloat16 if io == "bf16" else torch.float32) for _ in range(2))
+    zero = torch.zeros_like(q)
+    g = -80 * torch.rand((B, N, H), generator=r) / max(1, N / 2)
+    S, dS = (torch.randn((B, H, D, D), generator=r) for _ in range(2))
+    decay = np.exp(orc.to_f64(g).sum(1))[..., None, None]
+    got = la.gated_attention(*_dev(q, zero, zero, g), S_in=S.cuda(), want_state=True)[1]
+    want = decay * orc.to_f64(S)
+    normal = np.abs(want) > 2.0 ** -122
+    assert normal.mean() > 0.4 and (np.abs(orc.to_f64(got.cpu()) - want)[normal] <= 2.0 ** -20 * np.abs(want)[normal]).all()
+    got = la.gated_attention_backward(*_dev(zero, zero, zero, g, do), S_in=S.cuda(), dS_out=dS.cuda())[4]
+    want = decay * orc.to_f64(dS)
+    normal = np.abs(want) > 2.0 ** -122
+    assert normal.mean() > 0.4 and (np.abs(orc.to_f64(got.cpu()) - want)[normal] <= 2.0 ** -20 * np.abs(want)[normal]).all()
