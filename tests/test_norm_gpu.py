@@ -186,3 +186,27 @@ def test_empty_stream_and_graph(cuda_device):
     graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(p, q) for p, q in zip(held, call()))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("C,N", [(96, 40), (264, 1300), (2240, 1300), (2240, 9), (4096, 30)])
+def test_rows_are_apart(cuda_device, io, C, N):
+    """Rows that are not finite change no other row's bits, forwards or backwards, and no other
+    batch element's parameter gradients: a warp and a CTA a row, the next row ahead."""
+    t, dy, dh = _draw(3, N, C, io, 8, True, True)
+    d, dy, dh = _dev(t), dy.cuda(), dh.cuda()
+    par = {k: d[k] for k in ("gate", "w_post", "w_pre", "mod_scale", "mod_shift")}
+    call = lambda x, f, a, b: [*la.gate_residual_norm(x, f, **par, norm="layer"),  # noqa: E731
+                               *la.gate_residual_norm_backward(x, f, a, b, **par, norm="layer")]
+    want = call(d["x"], d["f"], dy, dh)
+    x, f, a, b = (y.clone() for y in (d["x"], d["f"], dy, dh))
+    rows = [2, N // 2, N - 2]
+    x[1, rows[0]], f[1, rows[1], 3], a[1, rows[2]] = float("nan"), float("inf"), float("nan")
+    got = call(x, f, a, b)
+    keep = torch.ones((3, N), dtype=torch.bool, device="cuda")
+    keep[1, rows] = False
+    for i in range(4):  # h, y, dx, df
+        assert torch.equal(got[i][keep], want[i][keep]), i
+    for i in (4, 7, 8):  # dgate, dmod_scale, dmod_shift
+        assert torch.equal(got[i][::2], want[i][::2]), i
+    assert got[7][1].isnan().all()
