@@ -74,7 +74,7 @@ __device__ __forceinline__ Decay<NP, NB> decays(const Known& known, float gate, 
 }
 // Two copies each: bf16 one without any of the three and one with all; float32 one for steps
 // with stops and one for the others, told apart by a vote, which the compiler knows to be the
-// same for the whole warp (3 x 2003 tokens of 36 heads: 69.5 us; by the stops' bits, and with
+// same for the whole warp (3 x 2003 tokens of 36 heads: 68 us; by the stops' bits, and with
 // their masks in the common copy too, 75 us).
 template <int NP, int NB, typename Step>
 __device__ __forceinline__ void run_step(float gate, bool ragged, int lane, const Step& step) {
