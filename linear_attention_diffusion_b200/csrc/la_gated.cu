@@ -37,8 +37,8 @@
 // backwards that carries U. dg is summed backwards from the two walks' float32 row
 // products, and set afresh to <U, S> every kGateAnchor tokens, where the first walk
 // has left its S: rounding errors of the sum do not grow with the length. At the size above
-// the four launches take 76, 6, 98 and 143 us by themselves; the walk backwards issues 114 products and 760
-// instructions a block, together 108 us if nothing overlapped.
+// the four launches take 76, 6, 98 and 143 us by themselves; the walk backwards issues 114 products
+// and 760 instructions a block, together 108 us if nothing overlapped.
 #include "la_gated.cuh"
 #include "la_sm100.cuh"
 
@@ -224,6 +224,7 @@ __device__ __forceinline__ void walk_pass(const Walk& a, const Place<kBlocks<NP>
     const int left = at.n_end - n0;
     auto step = [&](auto mode, auto known, uint32_t stops) {
       constexpr bool kStops = decltype(mode)::kStops, kLow = decltype(mode)::kLow;
+      constexpr bool kRagged = decltype(mode)::kRagged;
       uint32_t bad = 0;
       if (kStops && stops != 0)
         bad = take_out_gates<NB>(gate) | take_out<NP, NB>(st + M::kTile, st + 2 * M::kTile, lane);
@@ -252,8 +253,8 @@ __device__ __forceinline__ void walk_pass(const Walk& a, const Place<kBlocks<NP>
           Decay<NP, NB>::spread_rows(from_start, b, lane, r);
           scale_row<kStops>(acc[b], 0, r[0]);
           scale_row<kStops>(acc[b], 1, r[1]);
-          block_row<NP, NB, NC, true, kStops, kLow>(acc[b], b, q[b], tile[1], tile[2], plane, off, d, head,
-                                             tail, p.scale, lane);
+          block_row<NP, NB, NC, true, kStops, kLow>(acc[b], b, q[b], tile[1], tile[2], plane, off,
+                                                    d, head, tail, p.scale, lane);
           if (kStops && bad != 0)
             spoil_rows<NP, NB>(acc[b], b, spoiled_from(bad, stops, lane & (kStep - 1)), lane);
         }
@@ -284,8 +285,8 @@ __device__ __forceinline__ void walk_pass(const Walk& a, const Place<kBlocks<NP>
           }
           if ((lane & 3) == 0) {
             float* r = a.rows + static_cast<size_t>(at.bh) * p.N + n0 + b * kGateBlock + r0;
-            if (!decltype(mode)::kRagged || r0 + b * kGateBlock < left) r[0] = dots[0];
-            if (!decltype(mode)::kRagged || r0 + b * kGateBlock + 8 < left) r[8] = dots[1];
+            if (!kRagged || r0 + b * kGateBlock < left) r[0] = dots[0];
+            if (!kRagged || r0 + b * kGateBlock + 8 < left) r[8] = dots[1];
           }
         }
       }
@@ -293,7 +294,7 @@ __device__ __forceinline__ void walk_pass(const Walk& a, const Place<kBlocks<NP>
 #pragma unroll
       for (int b = 0; b < NB; ++b) Out<NP>::put(acc[b], st + b * M::kTile / NB, off, lane);
       __syncwarp();
-      out.template flush<kStep, !decltype(mode)::kRagged>(st, left, kStep, lane);
+      out.template flush<kStep, !kRagged>(st, left, kStep, lane);
     };
     run_step<NP, NB>(gate, left < kStep, lane, step);
   }
@@ -388,6 +389,7 @@ walk_back_kernel(const Walk a) {
     const int left = at.n_end - n0;
     auto step = [&](auto mode, auto known, uint32_t stops) {
       constexpr bool kStops = decltype(mode)::kStops, kLow = decltype(mode)::kLow;
+      constexpr bool kRagged = decltype(mode)::kRagged;
       uint32_t bad = 0;
       if (kStops && stops != 0)
         bad = take_out_gates<NB>(gate) | take_out<NP, NB>(st + 2 * M::kTile, st + 3 * M::kTile, lane);
@@ -445,7 +447,7 @@ walk_back_kernel(const Walk a) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) Out<NP>::put(acc[b], pass + b * M::kTile / NB, off, lane);
         __syncwarp();
-        (which == 0 ? out_k : out_v).template flush<kStep, !decltype(mode)::kRagged>(pass, left, -kStep, lane);
+        (which == 0 ? out_k : out_v).template flush<kStep, !kRagged>(pass, left, -kStep, lane);
       };
       side(Const<false>());
       side(Const<true>());
@@ -482,7 +484,7 @@ walk_back_kernel(const Walk a) {
       }
       float dg = after != 0 ? x : carry + x;
       if (kStops && ((stops >> i) & 1u)) dg = 0.0f;
-      if (lane < kStep && (!decltype(mode)::kRagged || i < left))
+      if (lane < kStep && (!kRagged || i < left))
         a.dG[at.gbase + static_cast<size_t>(n0 + i) * p.H] = dg;
       carry = __shfl_sync(0xffffffffu, dg, 0);
     };

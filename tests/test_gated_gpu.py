@@ -447,3 +447,31 @@ def test_what_passes_strong_gates_keeps_its_bits(cuda_device, io, N):
     want = decay * orc.to_f64(dS)
     normal = np.abs(want) > 2.0 ** -122
     assert normal.mean() > 0.4 and (np.abs(orc.to_f64(got.cpu()) - want)[normal] <= 2.0 ** -20 * np.abs(want)[normal]).all()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("B,N,H", [(2, 3, 3), (2, 40, 3), (1, 200, 60), (1, 1000, 2), (1, 60, 900)], ids=str)
+def test_states_that_are_not_finite_end_at_a_stop(cuda_device, io, B, N, H):
+    """A first state of NaN reaches no token from a stop on; backwards, the gradient of a last
+    state reaches none before it. Single tokens, a walk, a CTA per row, segments, uncut rows."""
+    q, k, v, g, do, S0, dS = _draw(B, N, H, io, 29)
+    stop = N // 2
+    g[:, stop] = -float("inf")
+    nan = torch.full_like(S0, float("nan"))
+    dev = _dev(q, k, v, g)
+    late = [x[:, stop:] for x in (q, k, v, g, do)]
+    O, S = la.gated_attention(*dev, S_in=nan.cuda(), want_state=True)
+    ref, S_ref = orc.gated_attention(*late[:4])
+    A, AS = orc.gated_magnitudes(*late[:4])
+    tol = _tol(io, N)
+    _check("O", O[:, stop:], ref, A, tol, HALF[io])
+    _check("S", S, S_ref, AS, tol, HALF["f32"])
+    for states, part in ((dict(S_in=nan, dS_out=dS), slice(stop, N)), (dict(S_in=S0, dS_out=nan), slice(0, stop))):
+        got = la.gated_attention_backward(*dev, do.cuda(), **{n: x.cuda() for n, x in states.items()})
+        cut = [x[:, part] for x in (q, k, v, g, do)]
+        ends = (None, dS) if part.start else (S0, None)
+        refs, mags = orc.gated_attention_backward(*cut, *ends), orc.gated_magnitudes(*cut, *ends)
+        for i, name in enumerate(("dQ", "dK", "dV", "dG")):
+            _check(name, got[i][:, part], refs[i], mags[i], 2 * tol, HALF[io] if i < 3 else HALF["f32"])
+        if not part.start:
+            _check("dS_in", got[4], refs[4], mags[4], tol, HALF["f32"])
